@@ -216,6 +216,64 @@ qbsa_status qbsa_quantize_v(const void* v_bf16, int B, int N, int S, int D, uint
 qbsa_status qbsa_quantize_v_noalloc(const void* v_bf16, int B, int N, int S, int D, uint8_t* codes, float* scales,
                                     void* stream);
 
+/* Element types of the W8A8 entry points below. */
+typedef enum { QBSA_BF16 = 0, QBSA_FP16 = 1, QBSA_FP32 = 2 } qbsa_dtype;
+
+/*
+ * qbsa_rms_norm_quant -- residual addition, root-mean-square norm and INT8 codes with one
+ * scale per token, in one pass: the input side of the 8-bit linear layers (W8A8) before and
+ * after the quantized attention.  The source pages quantise the attention only; the scale
+ * rule is the one of qbsa_quantize_qk, per row.  For every row:
+ *     h = x, or x + residual rounded to dtype (written to residual_out; the rounded sum is
+ *         what is normalised), g = h * weight in f32, a = max|g|,
+ *     s = max(a / 127, 2^-126) (1 if a = 0), codes = rint_half_even(g / s),
+ *     scale = s / sqrt(mean(h^2) + eps) (1 if a = 0), so that codes * scale is the normed row.
+ * The codes are rounded from g / s, which the norm's factor does not enter: they are
+ * reproducible bit for bit.  A row with a NaN or an infinity in g gets codes 0, scale NaN.
+ *   x, residual, residual_out   [rows, width] of dtype, with row strides in elements.
+ *               residual and residual_out are both given or both NULL; residual_out may be x
+ *               or residual itself (same row stride), and overlaps nothing otherwise.
+ *   weight      [width], of dtype or f32 (weight_dtype).
+ *   eps         finite, above 0.
+ *   codes       int8 [rows, width] with row stride codes_stride >= width.  What lies between
+ *               the rows is left as it was.  Rows that qbsa_matmul_i8 reads start at multiples
+ *               of 16 bytes.
+ *   scales      f32 [rows].
+ * Any alignment that the element type allows is taken; rows of all tensors on 16-byte
+ * boundaries (codes: 8 for 16-bit types, 4 for f32) run faster.  1 <= width <= 2^24;
+ * rows = 0 does nothing.  Asynchronous on `stream`, no scratch memory.
+ */
+qbsa_status qbsa_rms_norm_quant(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                const void* weight, qbsa_dtype dtype, qbsa_dtype weight_dtype, int64_t rows,
+                                int width, float eps, void* residual_out, int64_t residual_out_stride, int8_t* codes,
+                                int64_t codes_stride, float* scales, void* stream);
+
+/*
+ * qbsa_quantize_token -- the codes and scales of qbsa_rms_norm_quant without a norm: g = x,
+ * scale = s.  For activations that no norm precedes (the attention's output before its
+ * projection), and for weights [N, K], whose rows are the output channels.
+ */
+qbsa_status qbsa_quantize_token(const void* x, int64_t x_stride, qbsa_dtype dtype, int64_t rows, int width,
+                                int8_t* codes, int64_t codes_stride, float* scales, void* stream);
+
+/*
+ * qbsa_matmul_i8 -- product of INT8 codes with a scale for each token and each channel:
+ *     out[m, n] = (sum_k a[m, k] * b[n, k]) * a_scale[m] * b_scale[n] + bias[n]
+ * The sum is exact; it is rounded to f32, multiplied by a_scale[m], then by b_scale[n] with the
+ * bias added in the same rounding, and rounded to out_dtype.
+ *   a           int8 [M, K], b int8 [N, K] (both K-major), 16-byte aligned, row strides in
+ *               bytes, multiples of 16 (of no account for a single row).  Any code in
+ *               [-128, 127].  Bytes beyond K in a row are not used.
+ *   a_scale     f32 [M], b_scale f32 [N], bias f32 [N] or NULL.
+ *   out         [M, N] of out_dtype with row stride out_stride >= N in elements; overlaps no
+ *               input.  What lies between the rows is left as it was.
+ * 1 <= K <= 131071 (QBSA_ERR_UNSUPPORTED above: the sum would leave 32 bits); M = 0 or N = 0
+ * does nothing.  Asynchronous on `stream`, no scratch memory.
+ */
+qbsa_status qbsa_matmul_i8(const int8_t* a, int64_t a_stride, const int8_t* b, int64_t b_stride,
+                           const float* a_scale, const float* b_scale, const float* bias, int M, int N, int K,
+                           qbsa_dtype out_dtype, void* out, int64_t out_stride, void* stream);
+
 /*
  * attn_tile_schedule -- host-only export of the K-tile schedule attn_fwd's kernel uses
  * for one sequence under sparse_mode / pre_tokens / next_tokens ([NFA] §4.3): for each
@@ -300,7 +358,8 @@ const char* qbsa_last_error(void);
 
 /* Library ABI version (major * 100 + minor): 103 (1.01 added qbsa_block_mean, qbsa_block_topk,
  * qbsa_wait_selftest; 1.02 qbsa_block_topk_keep and qbsa_quantize_v_noalloc; 1.03
- * qbsa_fwd_host). */
+ * qbsa_fwd_host).  qbsa_rms_norm_quant, qbsa_quantize_token and qbsa_matmul_i8 only add
+ * symbols to 1.03; a caller that must know asks for the symbol. */
 int qbsa_version(void);
 
 #ifdef __cplusplus

@@ -28,9 +28,11 @@ Modules:
   quantized block-sparse forward, step by step in the article's order.
 * ``estimate`` -- block-mask estimation (block mean pooling, block scores, top-k), a plain
   reading of the block selection the EagleQBSA article names but does not describe.
+* ``linear8``  -- the 8-bit linear layers around the attention: token quantisers with and
+  without the RMS norm, and the INT8 product.
 
 Parity status of every function is stated in its docstring; none is "parity unpinned"
 except where a docstring says so.
 """
 
-from . import formats, dense, quant, estimate  # noqa: F401
+from . import formats, dense, quant, estimate, linear8  # noqa: F401

@@ -17,9 +17,12 @@ from ._binding import (  # noqa: F401
     estimate_block_mask,
     check,
     lib,
+    matmul_i8,
     qbsa_fwd,
     quantize_qk,
+    quantize_token,
     quantize_v,
+    rms_norm_quant,
 )
 
 from . import ulysses  # noqa: F401,E402  (sequence-parallel wrapper over torch.distributed)

@@ -33,6 +33,9 @@ SIGNATURES = {
     "qbsa_quantize_qk": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
     "qbsa_quantize_v": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
     "qbsa_quantize_v_noalloc": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "qbsa_rms_norm_quant": (_I, [_P, _I64, _P, _I64, _P, _I, _I, _I64, _I, _F, _P, _I64, _P, _I64, _P, _P]),
+    "qbsa_quantize_token": (_I, [_P, _I64, _I, _I64, _I, _P, _I64, _P, _P]),
+    "qbsa_matmul_i8": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _I, _I, _I, _I, _P, _I64, _P]),
     "attn_tile_schedule": (_I, [_I64, _I64, _I, _I64, _I64, _P, _P, _P, _P, _I64]),
     "qbsa_block_lists": (_I, [_P, _I64, _I, _P, _P, _P]),
     "qbsa_block_mean": (_I, [_P, _I, _I, _I, _I, _P, _P]),
@@ -283,6 +286,157 @@ def quantize_v(v):
     scales = torch.empty((B, N, D), dtype=torch.float32, device=v.device)
     _ck(lib().qbsa_quantize_v(_ptr(v), B, N, S, D, _ptr(codes), _ptr(scales), _stream(v.device)))
     return codes, scales
+
+
+def _dtype_code(dtype):
+    """The library's code of a float type, or None."""
+    import torch
+    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+
+
+def _rows(name, t, width=None, like=None):
+    """(row count, row stride) of a CUDA tensor [..., width] whose rows are contiguous and evenly spaced."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if like is not None and (t.device != like.device or t.dtype != like.dtype or t.shape != like.shape):
+        raise ValueError(f"{name} must have the shape, type and device that go with the input")
+    if t.dim() < 1 or (width is not None and t.shape[-1] != width):
+        raise ValueError(f"{name} must be [..., {width}]")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if t.dim() == 1:
+        return 1, t.shape[0]
+    if t.dim() == 2:
+        return t.shape[0], t.stride(0)
+    rows, stride = 1, 0
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if rows > 1 and n > 0 and st != stride * rows:
+            raise ValueError(f"{name}: its rows are not evenly spaced; make it contiguous")
+        if rows == 1:
+            stride = st
+        rows *= n
+    return rows, stride or t.shape[-1]
+
+
+def _vector(name, t, n, device, dtype):
+    import torch
+    if t.device != device or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on {device}")
+
+
+def _empty_codes(x):
+    """INT8 codes shaped as x, rows at multiples of 16 bytes (the layout matmul_i8 reads)."""
+    import torch
+    pitch = -(-x.shape[-1] // 16) * 16
+    codes = torch.empty((*x.shape[:-1], pitch), dtype=torch.int8, device=x.device)
+    return codes if pitch == x.shape[-1] else codes[..., :x.shape[-1]]
+
+
+def _call_on(device, fn, *args):
+    """A library call on `device`'s current stream, with that device current."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        _ck(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _ck(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _token_outputs(x, codes, scales):
+    import torch
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., width] with width >= 1")
+    if codes is None:
+        codes = _empty_codes(x)
+    elif codes.dtype != torch.int8 or codes.shape != x.shape or codes.device != x.device:
+        raise ValueError("codes must be an int8 tensor of x's shape on x's device")
+    n = x.numel() // x.shape[-1]
+    if scales is None:
+        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    else:
+        _vector("scales", scales, n, x.device, torch.float32)
+    return codes, scales
+
+
+def rms_norm_quant(x, weight, eps: float = 1e-6, *, residual=None, residual_out=None, codes=None, scales=None):
+    """Residual addition, RMS norm and INT8 codes with one scale per token: returns (codes, scales,
+    residual_out), where codes * scales is the norm of h = x + residual and residual_out is h in x's type
+    (None without a residual).
+
+    x, residual [..., width] bf16, fp16 or fp32 CUDA tensors with evenly spaced rows; weight [width] in x's
+    type or fp32.  residual_out may be x or residual itself.  New codes are laid out with rows at multiples
+    of 16 bytes, as matmul_i8 reads them."""
+    code = _dtype_code(x.dtype)
+    if code is None:
+        raise ValueError("x must be bfloat16, float16 or float32")
+    rows, xs = _rows("x", x)
+    codes, scales = _token_outputs(x, codes, scales)
+    width = x.shape[-1]
+    wcode = _dtype_code(weight.dtype)
+    if wcode is None or wcode not in (code, 2):
+        raise ValueError("weight must have x's type or float32")
+    _vector("weight", weight, width, x.device, weight.dtype)
+    rs = hs = 0
+    if residual is not None:
+        _, rs = _rows("residual", residual, width, like=x)
+        if residual_out is None:
+            import torch
+            residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _, hs = _rows("residual_out", residual_out, width, like=x)
+    elif residual_out is not None:
+        raise ValueError("residual_out is given with a residual only")
+    _, cs = _rows("codes", codes, width)
+    _call_on(x.device, lib().qbsa_rms_norm_quant, x.data_ptr(), xs, None if residual is None else residual.data_ptr(),
+             rs, weight.data_ptr(), code, wcode, rows, width, eps,
+             None if residual_out is None else residual_out.data_ptr(), hs, codes.data_ptr(), cs, scales.data_ptr())
+    return codes, scales, residual_out
+
+
+def quantize_token(x, *, codes=None, scales=None):
+    """INT8 codes and one fp32 scale per row of x [..., width] (bf16, fp16 or fp32): returns (codes, scales).
+    For activations without a norm, and for a weight [N, K], whose rows are the output channels."""
+    code = _dtype_code(x.dtype)
+    if code is None:
+        raise ValueError("x must be bfloat16, float16 or float32")
+    rows, xs = _rows("x", x)
+    codes, scales = _token_outputs(x, codes, scales)
+    _, cs = _rows("codes", codes)
+    _call_on(x.device, lib().qbsa_quantize_token, x.data_ptr(), xs, code, rows, x.shape[-1], codes.data_ptr(), cs,
+             scales.data_ptr())
+    return codes, scales
+
+
+def matmul_i8(a, b, a_scale, b_scale, *, bias=None, out_dtype=None, out=None):
+    """out[..., n] = (sum_k a[..., k] * b[n, k]) * a_scale * b_scale[n] + bias[n], the sum exact.
+
+    a [..., K] and b [N, K] int8 CUDA tensors (16-byte aligned, rows at multiples of 16 bytes, as the
+    quantisers lay them out), a_scale [...], b_scale [N] and bias [N] fp32.  out_dtype bf16 (default), fp16
+    or fp32; a given out [..., N] says it by its type."""
+    import torch
+    if a.dtype != torch.int8 or b.dtype != torch.int8 or b.dim() != 2 or a.device != b.device:
+        raise ValueError("a [..., K] and b [N, K] must be int8 tensors on one device")
+    m, sa = _rows("a", a)
+    n, sb = _rows("b", b, a.shape[-1])
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    code = _dtype_code(out_dtype)
+    if code is None or (out is not None and out.dtype != out_dtype):
+        raise ValueError("out_dtype must be bfloat16, float16 or float32, and out's type")
+    _vector("a_scale", a_scale, m, a.device, torch.float32)
+    _vector("b_scale", b_scale, n, a.device, torch.float32)
+    if bias is not None:
+        _vector("bias", bias, n, a.device, torch.float32)
+    shape = (*a.shape[:-1], n)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=a.device)
+    elif out.shape != shape or out.device != a.device:
+        raise ValueError(f"out must be {shape} on a's device")
+    _, so = _rows("out", out)
+    _call_on(a.device, lib().qbsa_matmul_i8, a.data_ptr(), sa, b.data_ptr(), sb, a_scale.data_ptr(),
+             b_scale.data_ptr(), None if bias is None else bias.data_ptr(), m, n, a.shape[-1], code, out.data_ptr(), so)
+    return out
 
 
 def attn_tile_schedule(sq: int, skv: int, sparse_mode: int = 0, pre_tokens: int = INF_TOKENS,

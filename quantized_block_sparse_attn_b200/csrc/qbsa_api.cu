@@ -19,6 +19,8 @@
 #include "attn_pair_masked.cuh"
 #include "attn_qbsa.cuh"
 #include "estimate.cuh"
+#include "matmul_i8.cuh"
+#include "norm_quant.cuh"
 #include "quantize.cuh"
 #include "schedule.cuh"
 
@@ -705,6 +707,186 @@ qbsa_status qbsa_quantize_v_noalloc(const void* v_bf16, int B, int N, int S, int
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync (V quantiser scratch)");
   prm.amax = w;
   return v_quant_launch(prm, D, s);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------
+// W8A8 layers: token quantisers and the INT8 product
+// ------------------------------------------------------------------------------
+
+namespace {
+
+int dtype_bytes(qbsa_dtype t) { return t == QBSA_FP32 ? 4 : 2; }
+bool known_dtype(qbsa_dtype t) { return t == QBSA_BF16 || t == QBSA_FP16 || t == QBSA_FP32; }
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+template <typename T, bool kNorm, bool kRes, int E, int kChunks>
+qbsa_status launch_norm_quant_as(const qbsa::NormQuantParams& prm, int threads, cudaStream_t s) {
+  const int rows_per_cta = prm.group <= 32 ? threads / prm.group : 1;
+  const int64_t grid = (prm.rows + rows_per_cta - 1) / rows_per_cta;
+  qbsa::norm_quant_kernel<T, kNorm, kRes, E, kChunks><<<dim3(static_cast<unsigned>(grid)), threads, 0, s>>>(prm);
+  return check_launch("norm_quant_kernel launch");
+}
+
+// Threads per row and values per thread by the row's number of pieces (16 bytes, or one value
+// where rows are not aligned).
+template <typename T, bool kNorm, bool kRes>
+qbsa_status launch_norm_quant(qbsa::NormQuantParams& prm, bool vec, cudaStream_t s) {
+  constexpr int E = 16 / sizeof(T);
+  const int pieces = vec ? (prm.width + E - 1) / E : prm.width;
+  const int per_warp = vec ? 64 : 32 * qbsa::kNormScalarValues;
+  if (pieces <= per_warp) {  // several rows per CTA of 8 warps
+    const int each = vec ? (pieces <= 32 ? 1 : 2) : qbsa::kNormScalarValues;
+    prm.group = 1;
+    while (prm.group * each < pieces) prm.group *= 2;
+    if (!vec) return launch_norm_quant_as<T, kNorm, kRes, 1, qbsa::kNormScalarValues>(prm, 256, s);
+    if (each == 1) return launch_norm_quant_as<T, kNorm, kRes, E, 1>(prm, 256, s);
+    return launch_norm_quant_as<T, kNorm, kRes, E, 2>(prm, 256, s);
+  }
+  const int each = vec ? (pieces <= 1024 ? 2 : 4) : qbsa::kNormScalarValues;
+  const int threads = ((pieces + each - 1) / each + 31) / 32 * 32;
+  prm.group = threads;
+  if (vec && each == 2) return launch_norm_quant_as<T, kNorm, kRes, E, 2>(prm, threads, s);
+  if (vec && threads <= 512) return launch_norm_quant_as<T, kNorm, kRes, E, 4>(prm, threads, s);
+  if (!vec && threads <= 1024)
+    return launch_norm_quant_as<T, kNorm, kRes, 1, qbsa::kNormScalarValues>(prm, threads, s);
+  const dim3 grid(static_cast<unsigned>(prm.rows));
+  if (vec) qbsa::norm_quant_wide_kernel<T, kNorm, kRes, E><<<grid, qbsa::kNormWideThreads, 0, s>>>(prm);
+  else qbsa::norm_quant_wide_kernel<T, kNorm, kRes, 1><<<grid, qbsa::kNormWideThreads, 0, s>>>(prm);
+  return check_launch("norm_quant_wide_kernel launch");
+}
+
+template <typename T>
+qbsa_status launch_norm_quant_type(qbsa::NormQuantParams& prm, bool vec, cudaStream_t s) {
+  if (!prm.weight) return launch_norm_quant<T, false, false>(prm, vec, s);
+  if (!prm.residual) return launch_norm_quant<T, true, false>(prm, vec, s);
+  return launch_norm_quant<T, true, true>(prm, vec, s);
+}
+
+// The checks and launch that qbsa_rms_norm_quant and qbsa_quantize_token share.
+qbsa_status norm_quant_impl(qbsa::NormQuantParams& prm, qbsa_dtype dtype, void* stream) {
+  if (prm.rows < 0 || prm.width < 1) return fail(QBSA_ERR_INVALID, "rows >= 0 and width >= 1");
+  if (prm.width > (1 << 24)) return fail(QBSA_ERR_UNSUPPORTED, "width above %d", 1 << 24);
+  if (prm.rows > 0x7fffffffLL) return fail(QBSA_ERR_UNSUPPORTED, "too many rows");
+  const int size = dtype_bytes(dtype);
+  if (!aligned_to(prm.x, size) || !aligned_to(prm.residual, size) || !aligned_to(prm.h_out, size) ||
+      !aligned_to(prm.scales, 4))
+    return fail(QBSA_ERR_INVALID, "tensors must be aligned to their element");
+  if (prm.rows > 1) {
+    if (prm.x_stride < 0 || prm.r_stride < 0) return fail(QBSA_ERR_INVALID, "row strides must not be negative");
+    if (prm.c_stride < prm.width || (prm.h_out && prm.h_stride < prm.width))
+      return fail(QBSA_ERR_INVALID, "output row strides must be at least the width");
+    if (prm.h_out && ((prm.h_out == prm.x && prm.h_stride != prm.x_stride) ||
+                      (prm.h_out == prm.residual && prm.h_stride != prm.r_stride)))
+      return fail(QBSA_ERR_INVALID, "residual_out in place needs the row stride of the tensor that it replaces");
+  }
+  if (prm.rows == 0) return QBSA_OK;
+  // rows by 16-byte pieces where every row of every tensor starts on such a boundary
+  const int piece = 16 / size;
+  auto rows16 = [&](const void* ptr, int64_t stride) {
+    return aligned16(ptr) && (prm.rows == 1 || stride % piece == 0);
+  };
+  const bool vec = rows16(prm.x, prm.x_stride) && rows16(prm.residual, prm.r_stride) &&
+                   rows16(prm.h_out, prm.h_stride) && aligned16(prm.weight) && aligned_to(prm.codes, piece) &&
+                   (prm.rows == 1 || prm.c_stride % piece == 0);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == QBSA_BF16) return launch_norm_quant_type<__nv_bfloat16>(prm, vec, s);
+  if (dtype == QBSA_FP16) return launch_norm_quant_type<__half>(prm, vec, s);
+  return launch_norm_quant_type<float>(prm, vec, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+qbsa_status qbsa_rms_norm_quant(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                const void* weight, qbsa_dtype dtype, qbsa_dtype weight_dtype, int64_t rows,
+                                int width, float eps, void* residual_out, int64_t residual_out_stride, int8_t* codes,
+                                int64_t codes_stride, float* scales, void* stream) {
+  if (!weight || (rows != 0 && (!x || !codes || !scales)))
+    return fail(QBSA_ERR_INVALID, "x, weight, codes and scales must be non-null");
+  if (!known_dtype(dtype)) return fail(QBSA_ERR_INVALID, "unknown dtype %d", (int)dtype);
+  if (weight_dtype != dtype && weight_dtype != QBSA_FP32)
+    return fail(QBSA_ERR_INVALID, "weight_dtype must be dtype or QBSA_FP32");
+  if (!aligned_to(weight, dtype_bytes(weight_dtype))) return fail(QBSA_ERR_INVALID, "weight is not aligned");
+  if (rows != 0 && (residual == nullptr) != (residual_out == nullptr))
+    return fail(QBSA_ERR_INVALID, "residual and residual_out are given together");
+  if (!std::isfinite(eps) || eps <= 0.f) return fail(QBSA_ERR_INVALID, "eps must be finite and above 0");
+  qbsa::NormQuantParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.x = x;
+  prm.residual = residual;
+  prm.weight = weight;
+  prm.h_out = residual_out;
+  prm.codes = codes;
+  prm.scales = scales;
+  prm.x_stride = x_stride;
+  prm.r_stride = residual_stride;
+  prm.h_stride = residual_out_stride;
+  prm.c_stride = codes_stride;
+  prm.rows = rows;
+  prm.width = width;
+  prm.weight_f32 = weight_dtype == QBSA_FP32;
+  prm.eps = eps;
+  return norm_quant_impl(prm, dtype, stream);
+}
+
+qbsa_status qbsa_quantize_token(const void* x, int64_t x_stride, qbsa_dtype dtype, int64_t rows, int width,
+                                int8_t* codes, int64_t codes_stride, float* scales, void* stream) {
+  if (rows != 0 && (!x || !codes || !scales)) return fail(QBSA_ERR_INVALID, "x, codes and scales must be non-null");
+  if (!known_dtype(dtype)) return fail(QBSA_ERR_INVALID, "unknown dtype %d", (int)dtype);
+  qbsa::NormQuantParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.x = x;
+  prm.codes = codes;
+  prm.scales = scales;
+  prm.x_stride = x_stride;
+  prm.c_stride = codes_stride;
+  prm.rows = rows;
+  prm.width = width;
+  return norm_quant_impl(prm, dtype, stream);
+}
+
+qbsa_status qbsa_matmul_i8(const int8_t* a, int64_t a_stride, const int8_t* b, int64_t b_stride,
+                           const float* a_scale, const float* b_scale, const float* bias, int M, int N, int K,
+                           qbsa_dtype out_dtype, void* out, int64_t out_stride, void* stream) {
+  if (M < 0 || N < 0 || K < 1) return fail(QBSA_ERR_INVALID, "M, N >= 0 and K >= 1");
+  if (!known_dtype(out_dtype)) return fail(QBSA_ERR_INVALID, "unknown out_dtype %d", (int)out_dtype);
+  if (K > qbsa::kMatmulMaxK) return fail(QBSA_ERR_UNSUPPORTED, "K above %d: the sum would leave 32 bits", qbsa::kMatmulMaxK);
+  if (M > kMaxLen || N > kMaxLen) return fail(QBSA_ERR_UNSUPPORTED, "M or N above %lld", (long long)kMaxLen);
+  if (M == 0 || N == 0) return QBSA_OK;
+  if (!a || !b || !a_scale || !b_scale || !out)
+    return fail(QBSA_ERR_INVALID, "a, b, a_scale, b_scale and out must be non-null");
+  if (!aligned16(a) || !aligned16(b)) return fail(QBSA_ERR_INVALID, "a and b must be 16-byte aligned");
+  if ((M > 1 && (a_stride < K || a_stride % 16 != 0)) || (N > 1 && (b_stride < K || b_stride % 16 != 0)))
+    return fail(QBSA_ERR_INVALID, "the row strides of a and b must be multiples of 16, at least K");
+  if (M > 1 && out_stride < N) return fail(QBSA_ERR_INVALID, "out_stride must be at least N");
+  if (!aligned_to(a_scale, 4) || !aligned_to(b_scale, 4) || !aligned_to(bias, 4) ||
+      !aligned_to(out, dtype_bytes(out_dtype)))
+    return fail(QBSA_ERR_INVALID, "scales, bias and out must be aligned to their element");
+  qbsa::MatmulI8Params prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.a = a;
+  prm.b = b;
+  prm.a_scale = a_scale;
+  prm.b_scale = b_scale;
+  prm.bias = bias;
+  prm.out = out;
+  prm.a_stride = a_stride;
+  prm.b_stride = b_stride;
+  prm.o_stride = out_stride;
+  prm.M = M;
+  prm.N = N;
+  prm.K = K;
+  const int64_t gm = ((int64_t)M + 63) / 64;
+  if (gm > 65535) return fail(QBSA_ERR_UNSUPPORTED, "too many rows");
+  const dim3 grid((N + 63) / 64, static_cast<unsigned>(gm));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (out_dtype == QBSA_BF16) qbsa::matmul_i8_simple_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(prm);
+  else if (out_dtype == QBSA_FP16) qbsa::matmul_i8_simple_kernel<__half><<<grid, 256, 0, s>>>(prm);
+  else qbsa::matmul_i8_simple_kernel<float><<<grid, 256, 0, s>>>(prm);
+  return check_launch("matmul_i8_simple_kernel launch");
 }
 
 }  // extern "C"
