@@ -1,6 +1,7 @@
 // C ABI of libqbsa.so: argument validation, TMA tensor maps and kernel launches.
 // The contract of every entry point is documented in include/qbsa.h.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -8,6 +9,7 @@
 #include <mutex>
 #include <numeric>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include <cuda.h>
@@ -764,6 +766,165 @@ qbsa_status launch_norm_quant_type(qbsa::NormQuantParams& prm, bool vec, cudaStr
   return launch_norm_quant<T, true, true>(prm, vec, s);
 }
 
+// Dynamic shared memory beyond 48 KB, asked for once per kernel and device.
+template <typename K>
+qbsa_status set_smem_once(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return QBSA_OK;
+  const qbsa_status st = set_smem(kernel, bytes);
+  if (st == QBSA_OK) done.fetch_or(bit, std::memory_order_relaxed);
+  return st;
+}
+
+// 2-D tiled map of `rows` rows of `inner` elements, box {box0, box1}, 128-byte swizzle.
+qbsa_status make_map_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t rows,
+                        uint64_t stride_bytes, uint32_t box0, uint32_t box1) {
+  EncodeTiledFn enc;
+  qbsa_status st = get_encoder(&enc);
+  if (st != QBSA_OK) return st;
+  const cuuint64_t gd[2] = {inner, rows}, gs[1] = {stride_bytes};
+  const cuuint32_t box[2] = {box0, box1}, es[2] = {1, 1};
+  const CUresult r = enc(map, dt, 2, const_cast<void*>(ptr), gd, gs, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(QBSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d; %llu x %llu, stride %llu)", (int)r,
+                (unsigned long long)rows, (unsigned long long)inner, (unsigned long long)stride_bytes);
+  return QBSA_OK;
+}
+
+qbsa_status sm_count(int* out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? QBSA_OK : cuda_fail(e, "cudaDeviceGetAttribute");
+}
+
+struct MatmulArgs {
+  const int8_t* a;
+  const int8_t* b;
+  const float* a_scale;
+  const float* b_scale;
+  const float* bias;
+  void* out;
+  int64_t a_stride, b_stride, o_stride;
+  int M, N, K;
+};
+
+template <typename O>
+constexpr CUtensorMapDataType map_type() {
+  return sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                        : std::is_same<O, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+template <typename O>
+qbsa_status matmul_i8_pair(const MatmulArgs& g, int sms, cudaStream_t s) {
+  using C = qbsa::MatmulPairCfg;
+  qbsa::MatmulPairParams prm;
+  memset(&prm, 0, sizeof(prm));
+  const int pairs = std::max(1, sms / 2);
+  prm.tiles_m = (g.M + 255) / 256;
+  int64_t best = INT64_MAX;
+  for (int bn = 256; bn >= 64; bn -= 32) {
+    if (128 % sizeof(O) != 0 || bn % (128 / sizeof(O)) != 0) continue;
+    const int64_t tiles = (int64_t)prm.tiles_m * ((g.N + bn - 1) / bn);
+    const int64_t cost = (tiles + pairs - 1) / pairs * (bn + 48);
+    if (cost < best) {
+      best = cost;
+      prm.BN = bn;
+    }
+  }
+  prm.tiles_n = (g.N + prm.BN - 1) / prm.BN;
+  prm.a_scale = g.a_scale;
+  prm.b_scale = g.b_scale;
+  prm.bias = g.bias;
+  prm.out = g.out;
+  prm.o_stride = g.o_stride;
+  prm.M = g.M;
+  prm.N = g.N;
+  prm.slabs = (g.K + 127) / 128;
+  qbsa_status st;
+  if ((st = make_map_2d(&prm.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.K, g.M, g.a_stride, 128, 128)) != QBSA_OK)
+    return st;
+  if ((st = make_map_2d(&prm.tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b, g.K, g.N, g.b_stride, 128, prm.BN / 2)) != QBSA_OK)
+    return st;
+  const uint64_t pitch = g.o_stride * sizeof(O);
+  prm.out_tma = aligned16(g.out) && pitch % 16 == 0;
+  if (prm.out_tma &&
+      (st = make_map_2d(&prm.tm_out, map_type<O>(), g.out, g.N, g.M, pitch, 128 / sizeof(O), 32)) != QBSA_OK)
+    return st;
+  static std::atomic<uint64_t> done{0};
+  if ((st = set_smem_once(qbsa::matmul_i8_pair_kernel<O>, C::kSmemBytes, done)) != QBSA_OK) return st;
+  const int64_t tiles = (int64_t)prm.tiles_m * prm.tiles_n;
+  const unsigned grid = 2u * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
+  qbsa::matmul_i8_pair_kernel<O><<<grid, C::kThreads, C::kSmemBytes, s>>>(prm);
+  return check_launch("matmul_i8_pair_kernel launch");
+}
+
+template <typename O>
+qbsa_status matmul_i8_split(const MatmulArgs& g, int sms, cudaStream_t s) {
+  using C = qbsa::MatmulSplitCfg;
+  qbsa::MatmulSplitParams prm;
+  memset(&prm, 0, sizeof(prm));
+  const int tiles_m = (g.M + 255) / 256;
+  prm.T = ((g.M + tiles_m - 1) / tiles_m + 15) / 16 * 16;
+  const int tiles_n = (g.N + 127) / 128;
+  prm.slabs = (g.K + 127) / 128;
+  prm.stage_bytes = C::kWBytes + prm.T * 128;
+  const int per_sm = prm.T <= 64 ? 2 : 1;
+  const int room = 232448 / per_sm - (per_sm > 1 ? 1024 : 0) - 1024 - C::kTailBytes;  // 1 KB a CTA is the system's
+  prm.stages = std::min(C::kMaxStages, room / prm.stage_bytes);
+  const int64_t tiles = (int64_t)tiles_m * tiles_n;
+  int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, (int64_t)sms * per_sm / tiles, prm.slabs})));
+  prm.slabs_per = (prm.slabs + splits - 1) / splits;
+  splits = (prm.slabs + prm.slabs_per - 1) / prm.slabs_per;
+  prm.tmem_cols = 32;
+  while (prm.tmem_cols < prm.T) prm.tmem_cols *= 2;
+  prm.a_scale = g.a_scale;
+  prm.b_scale = g.b_scale;
+  prm.bias = g.bias;
+  prm.out = g.out;
+  prm.o_stride = g.o_stride;
+  prm.M = g.M;
+  prm.N = g.N;
+  prm.vec = aligned_to(g.out, 4 * sizeof(O)) && (g.M == 1 || g.o_stride % 4 == 0);
+  if (tiles_n > 65535 || tiles_m > 65535) return fail(QBSA_ERR_UNSUPPORTED, "too many output tiles");
+  qbsa_status st;
+  if ((st = make_map_2d(&prm.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.K, g.M, g.a_stride, 128, prm.T)) != QBSA_OK)
+    return st;
+  if ((st = make_map_2d(&prm.tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b, g.K, g.N, g.b_stride, 128, 128)) != QBSA_OK)
+    return st;
+  static std::atomic<uint64_t> done{0};
+  if ((st = set_smem_once(qbsa::matmul_i8_split_kernel<O>, 232448, done)) != QBSA_OK) return st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(splits);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(splits, tiles_n, tiles_m);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = prm.stages * prm.stage_bytes + C::kTailBytes + 1024;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, qbsa::matmul_i8_split_kernel<O>, prm);
+  return e == cudaSuccess ? QBSA_OK : cuda_fail(e, "matmul_i8_split_kernel launch");
+}
+
+template <typename O>
+qbsa_status matmul_i8_launch(const MatmulArgs& g, cudaStream_t s) {
+  int sms = 0;
+  const qbsa_status st = sm_count(&sms);
+  if (st != QBSA_OK) return st;
+  return g.M <= 256 ? matmul_i8_split<O>(g, sms, s) : matmul_i8_pair<O>(g, sms, s);
+}
+
 // The checks and launch that qbsa_rms_norm_quant and qbsa_quantize_token share.
 qbsa_status norm_quant_impl(qbsa::NormQuantParams& prm, qbsa_dtype dtype, void* stream) {
   if (prm.rows < 0 || prm.width < 1) return fail(QBSA_ERR_INVALID, "rows >= 0 and width >= 1");
@@ -865,28 +1026,14 @@ qbsa_status qbsa_matmul_i8(const int8_t* a, int64_t a_stride, const int8_t* b, i
   if (!aligned_to(a_scale, 4) || !aligned_to(b_scale, 4) || !aligned_to(bias, 4) ||
       !aligned_to(out, dtype_bytes(out_dtype)))
     return fail(QBSA_ERR_INVALID, "scales, bias and out must be aligned to their element");
-  qbsa::MatmulI8Params prm;
-  memset(&prm, 0, sizeof(prm));
-  prm.a = a;
-  prm.b = b;
-  prm.a_scale = a_scale;
-  prm.b_scale = b_scale;
-  prm.bias = bias;
-  prm.out = out;
-  prm.a_stride = a_stride;
-  prm.b_stride = b_stride;
-  prm.o_stride = out_stride;
-  prm.M = M;
-  prm.N = N;
-  prm.K = K;
-  const int64_t gm = ((int64_t)M + 63) / 64;
-  if (gm > 65535) return fail(QBSA_ERR_UNSUPPORTED, "too many rows");
-  const dim3 grid((N + 63) / 64, static_cast<unsigned>(gm));
+  if ((int64_t)((M + 255) / 256) * ((N + 63) / 64) > 0x3fffffffLL)
+    return fail(QBSA_ERR_UNSUPPORTED, "too many output tiles");
+  MatmulArgs g = {a, b, a_scale, b_scale, bias, out, M > 1 ? a_stride : (K + 15) / 16 * 16,
+                  N > 1 ? b_stride : (K + 15) / 16 * 16, out_stride, M, N, K};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (out_dtype == QBSA_BF16) qbsa::matmul_i8_simple_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(prm);
-  else if (out_dtype == QBSA_FP16) qbsa::matmul_i8_simple_kernel<__half><<<grid, 256, 0, s>>>(prm);
-  else qbsa::matmul_i8_simple_kernel<float><<<grid, 256, 0, s>>>(prm);
-  return check_launch("matmul_i8_simple_kernel launch");
+  if (out_dtype == QBSA_BF16) return matmul_i8_launch<__nv_bfloat16>(g, s);
+  if (out_dtype == QBSA_FP16) return matmul_i8_launch<__half>(g, s);
+  return matmul_i8_launch<float>(g, s);
 }
 
 }  // extern "C"
