@@ -9,6 +9,7 @@ cannot run, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -288,76 +289,77 @@ def quantize_v(v):
     return codes, scales
 
 
+# The 8-bit linear layers below also run one token at a time, where the time is the host's: their
+# checks read each tensor's shape, strides, type and device once.
+
+@functools.lru_cache(maxsize=None)
 def _dtype_code(dtype):
     """The library's code of a float type, or None."""
     import torch
     return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
 
 
-def _rows(name, t, width=None, like=None):
-    """(row count, row stride) of a CUDA tensor [..., width] whose rows are contiguous and evenly spaced."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if like is not None and (t.device != like.device or t.dtype != like.dtype or t.shape != like.shape):
-        raise ValueError(f"{name} must have the shape, type and device that go with the input")
-    if t.dim() < 1 or (width is not None and t.shape[-1] != width):
-        raise ValueError(f"{name} must be [..., {width}]")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    if t.dim() == 1:
-        return 1, t.shape[0]
-    if t.dim() == 2:
-        return t.shape[0], t.stride(0)
-    rows, stride = 1, 0
-    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+def _rows(name, t):
+    """(row count, row stride) of a tensor [..., width] whose rows are contiguous and evenly spaced."""
+    shape, strides = t.shape, t.stride()
+    if not shape or (strides[-1] != 1 and shape[-1] > 1):
+        raise ValueError(f"{name} must be [..., width], contiguous in its last dimension")
+    if len(shape) == 2:
+        return shape[0], strides[0]
+    rows, stride = 1, shape[-1]
+    for n, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if n == 1:
             continue
-        if rows > 1 and n > 0 and st != stride * rows:
-            raise ValueError(f"{name}: its rows are not evenly spaced; make it contiguous")
         if rows == 1:
             stride = st
+        elif n > 0 and st != stride * rows:
+            raise ValueError(f"{name}: its rows are not evenly spaced; make it contiguous")
         rows *= n
-    return rows, stride or t.shape[-1]
+    return rows, stride
 
 
-def _vector(name, t, n, device, dtype):
+def _vector(name, t, n, dev, dtype):
+    if t.get_device() != dev or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on the input's device")
+
+
+def _call_on(dev, fn, *args):
+    """A library call on CUDA device `dev`'s current stream, with that device current."""
     import torch
-    if t.device != device or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on {device}")
-
-
-def _empty_codes(x):
-    """INT8 codes shaped as x, rows at multiples of 16 bytes (the layout matmul_i8 reads)."""
-    import torch
-    pitch = -(-x.shape[-1] // 16) * 16
-    codes = torch.empty((*x.shape[:-1], pitch), dtype=torch.int8, device=x.device)
-    return codes if pitch == x.shape[-1] else codes[..., :x.shape[-1]]
-
-
-def _call_on(device, fn, *args):
-    """A library call on `device`'s current stream, with that device current."""
-    import torch
-    if torch.cuda.current_device() == device.index:
-        _ck(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            _ck(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != 0:
+        _ck(status)
 
 
-def _token_outputs(x, codes, scales):
+def _token_arguments(x, codes, scales):
+    """Checks x and makes the outputs that were not given; codes get rows at multiples of 16 bytes, the layout
+    that matmul_i8 reads.  Returns (device, type code, codes, scales, rows, x's and codes' row strides)."""
     import torch
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("x must be [..., width] with width >= 1")
+    dev, shape, code = x.get_device(), x.shape, _dtype_code(x.dtype)
+    if dev < 0 or code is None or not shape or shape[-1] < 1:
+        raise ValueError("x must be a CUDA tensor [..., width] of bfloat16, float16 or float32, width >= 1")
+    rows, xs = _rows("x", x)
+    width = shape[-1]
     if codes is None:
-        codes = _empty_codes(x)
-    elif codes.dtype != torch.int8 or codes.shape != x.shape or codes.device != x.device:
-        raise ValueError("codes must be an int8 tensor of x's shape on x's device")
-    n = x.numel() // x.shape[-1]
-    if scales is None:
-        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        pitch = -(-width // 16) * 16
+        codes = x.new_empty((*shape[:-1], pitch), dtype=torch.int8)
+        if pitch != width:
+            codes = codes[..., :width]
+        cs = pitch
     else:
-        _vector("scales", scales, n, x.device, torch.float32)
-    return codes, scales
+        if codes.dtype != torch.int8 or codes.shape != shape or codes.get_device() != dev:
+            raise ValueError("codes must be an int8 tensor of x's shape on x's device")
+        cs = _rows("codes", codes)[1]
+    if scales is None:
+        scales = x.new_empty(shape[:-1], dtype=torch.float32)
+    else:
+        _vector("scales", scales, rows, dev, torch.float32)
+    return dev, code, codes, scales, rows, xs, cs
 
 
 def rms_norm_quant(x, weight, eps: float = 1e-6, *, residual=None, residual_out=None, codes=None, scales=None):
@@ -368,42 +370,33 @@ def rms_norm_quant(x, weight, eps: float = 1e-6, *, residual=None, residual_out=
     x, residual [..., width] bf16, fp16 or fp32 CUDA tensors with evenly spaced rows; weight [width] in x's
     type or fp32.  residual_out may be x or residual itself.  New codes are laid out with rows at multiples
     of 16 bytes, as matmul_i8 reads them."""
-    code = _dtype_code(x.dtype)
-    if code is None:
-        raise ValueError("x must be bfloat16, float16 or float32")
-    rows, xs = _rows("x", x)
-    codes, scales = _token_outputs(x, codes, scales)
+    dev, code, codes, scales, rows, xs, cs = _token_arguments(x, codes, scales)
     width = x.shape[-1]
     wcode = _dtype_code(weight.dtype)
-    if wcode is None or wcode not in (code, 2):
+    if wcode != code and wcode != 2:
         raise ValueError("weight must have x's type or float32")
-    _vector("weight", weight, width, x.device, weight.dtype)
-    rs = hs = 0
+    _vector("weight", weight, width, dev, weight.dtype)
+    r_ptr, rs, h_ptr, hs = None, 0, None, 0
     if residual is not None:
-        _, rs = _rows("residual", residual, width, like=x)
         if residual_out is None:
-            import torch
-            residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        _, hs = _rows("residual_out", residual_out, width, like=x)
+            residual_out = x.new_empty(x.shape)
+        for name, t in (("residual", residual), ("residual_out", residual_out)):
+            if t.dtype != x.dtype or t.shape != x.shape or t.get_device() != dev:
+                raise ValueError(f"{name} must have x's shape, type and device")
+        r_ptr, rs = residual.data_ptr(), _rows("residual", residual)[1]
+        h_ptr, hs = residual_out.data_ptr(), _rows("residual_out", residual_out)[1]
     elif residual_out is not None:
         raise ValueError("residual_out is given with a residual only")
-    _, cs = _rows("codes", codes, width)
-    _call_on(x.device, lib().qbsa_rms_norm_quant, x.data_ptr(), xs, None if residual is None else residual.data_ptr(),
-             rs, weight.data_ptr(), code, wcode, rows, width, eps,
-             None if residual_out is None else residual_out.data_ptr(), hs, codes.data_ptr(), cs, scales.data_ptr())
+    _call_on(dev, lib().qbsa_rms_norm_quant, x.data_ptr(), xs, r_ptr, rs, weight.data_ptr(), code, wcode, rows, width,
+             eps, h_ptr, hs, codes.data_ptr(), cs, scales.data_ptr())
     return codes, scales, residual_out
 
 
 def quantize_token(x, *, codes=None, scales=None):
     """INT8 codes and one fp32 scale per row of x [..., width] (bf16, fp16 or fp32): returns (codes, scales).
     For activations without a norm, and for a weight [N, K], whose rows are the output channels."""
-    code = _dtype_code(x.dtype)
-    if code is None:
-        raise ValueError("x must be bfloat16, float16 or float32")
-    rows, xs = _rows("x", x)
-    codes, scales = _token_outputs(x, codes, scales)
-    _, cs = _rows("codes", codes)
-    _call_on(x.device, lib().qbsa_quantize_token, x.data_ptr(), xs, code, rows, x.shape[-1], codes.data_ptr(), cs,
+    dev, code, codes, scales, rows, xs, cs = _token_arguments(x, codes, scales)
+    _call_on(dev, lib().qbsa_quantize_token, x.data_ptr(), xs, code, rows, x.shape[-1], codes.data_ptr(), cs,
              scales.data_ptr())
     return codes, scales
 
@@ -415,27 +408,34 @@ def matmul_i8(a, b, a_scale, b_scale, *, bias=None, out_dtype=None, out=None):
     quantisers lay them out), a_scale [...], b_scale [N] and bias [N] fp32.  out_dtype bf16 (default), fp16
     or fp32; a given out [..., N] says it by its type."""
     import torch
-    if a.dtype != torch.int8 or b.dtype != torch.int8 or b.dim() != 2 or a.device != b.device:
-        raise ValueError("a [..., K] and b [N, K] must be int8 tensors on one device")
+    dev, a_shape, b_shape = a.get_device(), a.shape, b.shape
+    if dev < 0 or b.get_device() != dev or a.dtype != torch.int8 or b.dtype != torch.int8:
+        raise ValueError("a and b must be int8 tensors on one CUDA device")
+    if len(b_shape) != 2 or not a_shape or a_shape[-1] != b_shape[1]:
+        raise ValueError("a must be [..., K] and b [N, K]")
     m, sa = _rows("a", a)
-    n, sb = _rows("b", b, a.shape[-1])
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if out is None else out.dtype
-    code = _dtype_code(out_dtype)
-    if code is None or (out is not None and out.dtype != out_dtype):
-        raise ValueError("out_dtype must be bfloat16, float16 or float32, and out's type")
-    _vector("a_scale", a_scale, m, a.device, torch.float32)
-    _vector("b_scale", b_scale, n, a.device, torch.float32)
+    n, sb = _rows("b", b)
+    f32 = torch.float32
+    _vector("a_scale", a_scale, m, dev, f32)
+    _vector("b_scale", b_scale, n, dev, f32)
     if bias is not None:
-        _vector("bias", bias, n, a.device, torch.float32)
-    shape = (*a.shape[:-1], n)
+        _vector("bias", bias, n, dev, f32)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=a.device)
-    elif out.shape != shape or out.device != a.device:
-        raise ValueError(f"out must be {shape} on a's device")
-    _, so = _rows("out", out)
-    _call_on(a.device, lib().qbsa_matmul_i8, a.data_ptr(), sa, b.data_ptr(), sb, a_scale.data_ptr(),
-             b_scale.data_ptr(), None if bias is None else bias.data_ptr(), m, n, a.shape[-1], code, out.data_ptr(), so)
+        if out_dtype is None:
+            out_dtype = torch.bfloat16
+        code = _dtype_code(out_dtype)
+        if code is None:
+            raise ValueError("out_dtype must be bfloat16, float16 or float32")
+        out, so = a.new_empty((*a_shape[:-1], n), dtype=out_dtype), n
+    else:
+        code = _dtype_code(out.dtype)
+        if code is None or out_dtype not in (None, out.dtype):
+            raise ValueError("out must be bfloat16, float16 or float32, and of out_dtype")
+        if out.shape != (*a_shape[:-1], n) or out.get_device() != dev:
+            raise ValueError("out must be [..., N] on a's device")
+        so = _rows("out", out)[1]
+    _call_on(dev, lib().qbsa_matmul_i8, a.data_ptr(), sa, b.data_ptr(), sb, a_scale.data_ptr(), b_scale.data_ptr(),
+             None if bias is None else bias.data_ptr(), m, n, a_shape[-1], code, out.data_ptr(), so)
     return out
 
 

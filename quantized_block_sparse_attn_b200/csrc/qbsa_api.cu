@@ -719,53 +719,6 @@ qbsa_status qbsa_quantize_v_noalloc(const void* v_bf16, int B, int N, int S, int
 
 namespace {
 
-int dtype_bytes(qbsa_dtype t) { return t == QBSA_FP32 ? 4 : 2; }
-bool known_dtype(qbsa_dtype t) { return t == QBSA_BF16 || t == QBSA_FP16 || t == QBSA_FP32; }
-bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
-
-template <typename T, bool kNorm, bool kRes, int E, int kChunks>
-qbsa_status launch_norm_quant_as(const qbsa::NormQuantParams& prm, int threads, cudaStream_t s) {
-  const int rows_per_cta = prm.group <= 32 ? threads / prm.group : 1;
-  const int64_t grid = (prm.rows + rows_per_cta - 1) / rows_per_cta;
-  qbsa::norm_quant_kernel<T, kNorm, kRes, E, kChunks><<<dim3(static_cast<unsigned>(grid)), threads, 0, s>>>(prm);
-  return check_launch("norm_quant_kernel launch");
-}
-
-// Threads per row and values per thread by the row's number of pieces (16 bytes, or one value
-// where rows are not aligned).
-template <typename T, bool kNorm, bool kRes>
-qbsa_status launch_norm_quant(qbsa::NormQuantParams& prm, bool vec, cudaStream_t s) {
-  constexpr int E = 16 / sizeof(T);
-  const int pieces = vec ? (prm.width + E - 1) / E : prm.width;
-  const int per_warp = vec ? 64 : 32 * qbsa::kNormScalarValues;
-  if (pieces <= per_warp) {  // several rows per CTA of 8 warps
-    const int each = vec ? (pieces <= 32 ? 1 : 2) : qbsa::kNormScalarValues;
-    prm.group = 1;
-    while (prm.group * each < pieces) prm.group *= 2;
-    if (!vec) return launch_norm_quant_as<T, kNorm, kRes, 1, qbsa::kNormScalarValues>(prm, 256, s);
-    if (each == 1) return launch_norm_quant_as<T, kNorm, kRes, E, 1>(prm, 256, s);
-    return launch_norm_quant_as<T, kNorm, kRes, E, 2>(prm, 256, s);
-  }
-  const int each = vec ? (pieces <= 1024 ? 2 : 4) : qbsa::kNormScalarValues;
-  const int threads = ((pieces + each - 1) / each + 31) / 32 * 32;
-  prm.group = threads;
-  if (vec && each == 2) return launch_norm_quant_as<T, kNorm, kRes, E, 2>(prm, threads, s);
-  if (vec && threads <= 512) return launch_norm_quant_as<T, kNorm, kRes, E, 4>(prm, threads, s);
-  if (!vec && threads <= 1024)
-    return launch_norm_quant_as<T, kNorm, kRes, 1, qbsa::kNormScalarValues>(prm, threads, s);
-  const dim3 grid(static_cast<unsigned>(prm.rows));
-  if (vec) qbsa::norm_quant_wide_kernel<T, kNorm, kRes, E><<<grid, qbsa::kNormWideThreads, 0, s>>>(prm);
-  else qbsa::norm_quant_wide_kernel<T, kNorm, kRes, 1><<<grid, qbsa::kNormWideThreads, 0, s>>>(prm);
-  return check_launch("norm_quant_wide_kernel launch");
-}
-
-template <typename T>
-qbsa_status launch_norm_quant_type(qbsa::NormQuantParams& prm, bool vec, cudaStream_t s) {
-  if (!prm.weight) return launch_norm_quant<T, false, false>(prm, vec, s);
-  if (!prm.residual) return launch_norm_quant<T, true, false>(prm, vec, s);
-  return launch_norm_quant<T, true, true>(prm, vec, s);
-}
-
 // Dynamic shared memory beyond 48 KB, asked for once per kernel and device.
 template <typename K>
 qbsa_status set_smem_once(K kernel, int bytes, std::atomic<uint64_t>& done) {
@@ -801,6 +754,90 @@ qbsa_status sm_count(int* out) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
   return e == cudaSuccess ? QBSA_OK : cuda_fail(e, "cudaDeviceGetAttribute");
+}
+
+int dtype_bytes(qbsa_dtype t) { return t == QBSA_FP32 ? 4 : 2; }
+bool known_dtype(qbsa_dtype t) { return t == QBSA_BF16 || t == QBSA_FP16 || t == QBSA_FP32; }
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+constexpr int kNormRingBytes = 216 * 1024;  // of an SM's shared memory, over its resident CTAs
+
+template <typename T, bool kNorm, bool kRes, int E, int kChunks, int kRows>
+qbsa_status launch_norm_rows(const qbsa::NormQuantParams& prm, cudaStream_t s) {
+  const int64_t rows_per_cta = 256 / prm.group * kRows;
+  const int64_t grid = (prm.rows + rows_per_cta - 1) / rows_per_cta;
+  qbsa::norm_quant_rows_kernel<T, kNorm, kRes, E, kChunks, kRows><<<static_cast<unsigned>(grid), 256, 0, s>>>(prm);
+  return check_launch("norm_quant_rows_kernel launch");
+}
+
+// Resident CTAs that stream rows of up to 640 x 4 pieces, when there are more rows than such CTAs
+// run at once.  *taken says whether it was launched.
+template <typename T, bool kNorm, bool kRes, int kChunks, bool kAligned>
+qbsa_status launch_norm_stream(qbsa::NormQuantParams& prm, int threads, cudaStream_t s, bool* taken) {
+  int sms = 0;
+  qbsa_status st = sm_count(&sms);
+  if (st != QBSA_OK) return st;
+  const int64_t slot = qbsa::stream_slot_bytes<T>(prm.width, kAligned);
+  const int64_t stage = slot * (kRes ? 2 : 1), staged = kRes && !kAligned ? 2 * slot : 0;
+  int per_sm = std::max(1, std::min(16, (kChunks == 2 ? 1024 : 682) / threads));  // 64 or 96 registers
+  while (per_sm > 1 && (2 * stage + staged) * per_sm > kNormRingBytes) --per_sm;
+  prm.stages = static_cast<int>(std::min<int64_t>(qbsa::kNormMaxStages, (kNormRingBytes / per_sm - staged) / stage));
+  if (prm.stages < 2 || prm.rows <= (int64_t)sms * per_sm) return QBSA_OK;
+  if (!kAligned && (prm.x_stride < prm.width || (kRes && prm.r_stride < prm.width))) return QBSA_OK;
+  const auto kernel = qbsa::norm_quant_stream_kernel<T, kNorm, kRes, kChunks, kAligned>;
+  static std::atomic<uint64_t> done{0};
+  if ((st = set_smem_once(kernel, kNormRingBytes, done)) != QBSA_OK) return st;
+  kernel<<<static_cast<unsigned>(sms) * per_sm, threads, static_cast<size_t>(prm.stages * stage + staged), s>>>(prm);
+  *taken = true;
+  return check_launch("norm_quant_stream_kernel launch");
+}
+
+template <typename T, bool kNorm, bool kRes, int E, int kChunks>
+qbsa_status launch_norm_cta(const qbsa::NormQuantParams& prm, int threads, cudaStream_t s) {
+  qbsa::norm_quant_kernel<T, kNorm, kRes, E, kChunks><<<static_cast<unsigned>(prm.rows), threads, 0, s>>>(prm);
+  return check_launch("norm_quant_kernel launch");
+}
+
+// Threads per row and values per thread by the row's number of pieces (16 bytes, or one value
+// where rows are not aligned).
+template <typename T, bool kNorm, bool kRes>
+qbsa_status launch_norm_quant(qbsa::NormQuantParams& prm, bool vec, cudaStream_t s) {
+  constexpr int E = 16 / sizeof(T);
+  const int pieces = (prm.width + E - 1) / E;
+  auto threads = [](int values, int each) { return ((values + each - 1) / each + 31) / 32 * 32; };
+  if (vec ? pieces <= 64 : prm.width <= 256) {  // several rows per CTA
+    const int each = !vec ? 8 : pieces <= 32 ? 1 : 2;
+    prm.group = 1;
+    while (prm.group * each < (vec ? pieces : prm.width)) prm.group *= 2;
+    if (!vec) return launch_norm_rows<T, kNorm, kRes, 1, 8, 1>(prm, s);
+    if (each == 1) return launch_norm_rows<T, kNorm, kRes, E, 1, 4>(prm, s);
+    return launch_norm_rows<T, kNorm, kRes, E, 2, 2>(prm, s);
+  }
+  bool taken = false;
+  if (pieces <= 2560) {
+    const bool aligned = vec && prm.width % E == 0;
+    const int each = pieces <= 1024 ? 2 : 4, n = threads(pieces, each);
+    const qbsa_status st =
+        each == 2 ? (aligned ? launch_norm_stream<T, kNorm, kRes, 2, true>(prm, n, s, &taken)
+                             : launch_norm_stream<T, kNorm, kRes, 2, false>(prm, n, s, &taken))
+                  : (aligned ? launch_norm_stream<T, kNorm, kRes, 4, true>(prm, n, s, &taken)
+                             : launch_norm_stream<T, kNorm, kRes, 4, false>(prm, n, s, &taken));
+    if (taken || st != QBSA_OK) return st;
+    if (vec && each == 2) return launch_norm_cta<T, kNorm, kRes, E, 2>(prm, n, s);
+    if (vec) return launch_norm_cta<T, kNorm, kRes, E, 4>(prm, n, s);
+    if (prm.width <= 8192) return launch_norm_cta<T, kNorm, kRes, 1, 8>(prm, threads(prm.width, 8), s);
+  }
+  const dim3 grid(static_cast<unsigned>(prm.rows));
+  if (vec) qbsa::norm_quant_wide_kernel<T, kNorm, kRes, E><<<grid, qbsa::kNormWideThreads, 0, s>>>(prm);
+  else qbsa::norm_quant_wide_kernel<T, kNorm, kRes, 1><<<grid, qbsa::kNormWideThreads, 0, s>>>(prm);
+  return check_launch("norm_quant_wide_kernel launch");
+}
+
+template <typename T>
+qbsa_status launch_norm_quant_type(qbsa::NormQuantParams& prm, bool vec, cudaStream_t s) {
+  if (!prm.weight) return launch_norm_quant<T, false, false>(prm, vec, s);
+  if (!prm.residual) return launch_norm_quant<T, true, false>(prm, vec, s);
+  return launch_norm_quant<T, true, true>(prm, vec, s);
 }
 
 struct MatmulArgs {
@@ -948,9 +985,10 @@ qbsa_status norm_quant_impl(qbsa::NormQuantParams& prm, qbsa_dtype dtype, void* 
   auto rows16 = [&](const void* ptr, int64_t stride) {
     return aligned16(ptr) && (prm.rows == 1 || stride % piece == 0);
   };
+  prm.weight_vec = aligned16(prm.weight);
+  prm.codes_vec = aligned_to(prm.codes, piece) && (prm.rows == 1 || prm.c_stride % piece == 0);
   const bool vec = rows16(prm.x, prm.x_stride) && rows16(prm.residual, prm.r_stride) &&
-                   rows16(prm.h_out, prm.h_stride) && aligned16(prm.weight) && aligned_to(prm.codes, piece) &&
-                   (prm.rows == 1 || prm.c_stride % piece == 0);
+                   rows16(prm.h_out, prm.h_stride) && prm.weight_vec && prm.codes_vec;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == QBSA_BF16) return launch_norm_quant_type<__nv_bfloat16>(prm, vec, s);
   if (dtype == QBSA_FP16) return launch_norm_quant_type<__half>(prm, vec, s);

@@ -89,6 +89,55 @@ def test_row_counts(rows):
         _check_tokens(codes, scales, x, w, 1e-6)
 
 
+@pytest.mark.parametrize("width", [128, 130, 264, 512, 513, 520, 1024, 1031, 2047, 4096, 5120, 8193, 12000, 20480, 20481])
+@pytest.mark.parametrize("dtype,residual", [(BF16, True), (BF16, False), (FP16, True), (FP32, True), (FP32, False)])
+def test_more_rows_than_run_at_once(width, dtype, residual):
+    """Rows past one per resident CTA (streamed through shared memory), from tensors that start and end
+    off a 16-byte boundary where the width is odd; with and without a norm."""
+    rows = 2500 if width <= 5120 else 500
+    pool = _randn(width, (rows * width + 3,), dtype)
+    off = 3 if width % 8 else 0
+    x = pool[off:off + rows * width].view(rows, width)
+    res = _randn(width + 1, (rows, width), dtype) if residual else None
+    w = _randn(width + 2, (width,), dtype)
+    keep = pool.clone()
+    codes, scales, h = qb.rms_norm_quant(x, w, residual=res)
+    qb.check()
+    assert torch.equal(pool, keep)
+    if residual:
+        assert torch.equal(h, (x.float() + res.float()).to(dtype))
+    _check_tokens(codes, scales, h if residual else x, w, 1e-6)
+    if residual:                                          # in place, and the squares of one row overflow
+        if dtype != FP16:
+            x[rows // 2] *= 1e30
+        h = (x.float() + res.float()).to(dtype)
+        codes, scales, got = qb.rms_norm_quant(x, w, residual=res, residual_out=x)
+        assert got.data_ptr() == x.data_ptr() and torch.equal(x, h)
+        assert torch.equal(pool[:off], keep[:off]) and torch.equal(pool[off + rows * width:], keep[off + rows * width:])
+        _check_tokens(codes, scales, h, w, 1e-6)
+    else:
+        codes, scales = qb.quantize_token(x)
+        _check_tokens(codes, scales, x)
+    qb.check()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_every_short_quotient(dtype):
+    """Rows of a 16-bit type whose largest value takes every significand, with every smaller significand at
+    every exponent that reaches a code: half-integer quotients among them."""
+    bits = 7 if dtype == BF16 else 10
+    n = 1 << bits
+    tops = torch.arange(n, 2 * n, device="cuda", dtype=torch.float32)
+    if dtype == FP16:
+        tops = tops[::8]
+    all_x = torch.cat([torch.arange(n, 2 * n, device="cuda", dtype=torch.float32) * 2.0 ** -j for j in range(9)])
+    for scale in (1.0, 2.0 ** -8, 2.0 ** 5) if dtype == FP16 else (1.0, 2.0 ** -100, 2.0 ** 100):
+        rows = torch.where(all_x[None] <= tops[:, None], all_x[None], torch.zeros((), device="cuda"))
+        rows = (torch.cat([tops[:, None], rows], 1) * scale).to(dtype)
+        codes, scales = qb.quantize_token(rows)
+        _check_tokens(codes, scales, rows)
+
+
 @pytest.mark.parametrize("width,off,pitch", [(64, 0, 80), (64, 1, 80), (130, 0, 136), (130, 3, 137), (1024, 8, 2048),
                                              (1024, 5, 1031), (5120, 0, 5128)])
 @pytest.mark.parametrize("dtype", [BF16, FP32])

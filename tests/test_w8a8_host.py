@@ -148,3 +148,26 @@ def test_oracle_product_by_loops():
         for n in range(2):
             want = sum(int(a[m, k]) * int(b[n, k]) for k in range(7)) * sa[m] * sb[n] + bias[n]
             assert abs(out[m, n] - want) <= 1e-9 * max(1, abs(want))
+
+
+@pytest.mark.parametrize("bits", [7, 10])
+def test_short_quotients_by_a_reciprocal_in_two_parts(bits):
+    """The kernel's quotient of 16-bit values, FMA(x, r, RN(x r_low)) with r = RN(1 / s) and
+    r_low = RN(r RN(1 - s r)), equals the division RN(x / s), s = RN(a / 127), for every pair of significands
+    (7 stored bits: bf16, 10: fp16) and every ratio that reaches a code; codes are equal with it."""
+    f, g = np.float32, np.longdouble
+    n = 1 << bits
+    sig = np.arange(n, 2 * n).astype(f)
+    xs = np.concatenate([sig * f(2.0 ** -j) for j in range(9)])
+    assert np.finfo(g).nmant >= 63
+    for a in sig[:: 1 if bits == 7 else 4]:
+        s = f(a / f(127))
+        r = f(f(1) / s)
+        r_low = f(f(g(1) - g(s) * g(r)) * r)
+        x = xs[xs <= a]
+        y = (x.astype(g) * g(r) + (x * r_low).astype(g)).astype(f)     # 11 + 24 and 24 bits: exact in g
+        want = x / s
+        assert np.array_equal(y, want)
+        assert np.array_equal(np.rint(y), np.rint(want))
+    # smaller values round to 0
+    assert n * 2.0 ** -8 / (n / 127) < 0.5
