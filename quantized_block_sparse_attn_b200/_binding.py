@@ -346,17 +346,17 @@ def _token_arguments(x, codes, scales):
     rows, xs = _rows("x", x)
     width = shape[-1]
     if codes is None:
-        pitch = -(-width // 16) * 16
-        codes = x.new_empty((*shape[:-1], pitch), dtype=torch.int8)
-        if pitch != width:
-            codes = codes[..., :width]
-        cs = pitch
+        if width % 16 == 0 and x.is_contiguous():
+            codes, cs = torch.empty_like(x, dtype=torch.int8), width
+        else:
+            cs = -(-width // 16) * 16
+            codes = x.new_empty((*shape[:-1], cs), dtype=torch.int8)[..., :width]
     else:
         if codes.dtype != torch.int8 or codes.shape != shape or codes.get_device() != dev:
             raise ValueError("codes must be an int8 tensor of x's shape on x's device")
         cs = _rows("codes", codes)[1]
     if scales is None:
-        scales = x.new_empty(shape[:-1], dtype=torch.float32)
+        scales = x.new_empty(rows if len(shape) == 2 else shape[:-1], dtype=torch.float32)
     else:
         _vector("scales", scales, rows, dev, torch.float32)
     return dev, code, codes, scales, rows, xs, cs
@@ -379,7 +379,8 @@ def rms_norm_quant(x, weight, eps: float = 1e-6, *, residual=None, residual_out=
     r_ptr, rs, h_ptr, hs = None, 0, None, 0
     if residual is not None:
         if residual_out is None:
-            residual_out = x.new_empty(x.shape)
+            import torch
+            residual_out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
         for name, t in (("residual", residual), ("residual_out", residual_out)):
             if t.dtype != x.dtype or t.shape != x.shape or t.get_device() != dev:
                 raise ValueError(f"{name} must have x's shape, type and device")

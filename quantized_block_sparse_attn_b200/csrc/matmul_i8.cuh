@@ -354,6 +354,25 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
   const int n0 = blockIdx.y * 128, m0 = blockIdx.z * p.T;
   const int k0 = rank * p.slabs_per, slabs = min(p.slabs_per, p.slabs - k0);
 
+  // this lane's channels and this warp's first token: fetched while the sums are made
+  const int n = n0 + 4 * lane, tokens = min(p.T, p.M - m0);
+  float sb[4], bi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sb[i] = n + i < p.N ? p.b_scale[n + i] : 0.f;
+    bi[i] = n + i < p.N && p.bias ? p.bias[n + i] : 0.f;
+  }
+  float sa = rank + splits * warp < tokens ? p.a_scale[m0 + rank + splits * warp] : 0.f;
+  bool acc_ok = false;
+
+  const uint64_t pol_w = l2_policy_evict_first(), pol_t = l2_policy_evict_last();
+  auto load = [&](int it) {  // slab `it` of this CTA into its stage
+    const int s = it % p.stages;
+    mbar_arrive_expect_tx(bar(C::kBarFull + s), p.stage_bytes);
+    const uint32_t dst = base + s * p.stage_bytes;
+    tma_load_2d(dst, &p.tm_b, bar(C::kBarFull + s), (k0 + it) * 128, n0, pol_w);
+    tma_load_2d(dst + C::kWBytes, &p.tm_a, bar(C::kBarFull + s), (k0 + it) * 128, m0, pol_t);
+  };
   if (warp == 4 && lane == 0) {
     *abort_flag = 0;
     for (int s = 0; s < p.stages; ++s) {
@@ -362,6 +381,7 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
     }
     mbar_init(bar(C::kBarAccFull), 1);
     fence_mbar_init();
+    for (int it = 0; it < min(p.stages, slabs); ++it) load(it);  // under way while TMEM is allocated
   } else if (warp == 5) {
     tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
     tmem_relinquish();
@@ -375,17 +395,11 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
     if (lane == 0) {
-      const uint64_t pol_w = l2_policy_evict_first(), pol_t = l2_policy_evict_last();
-      int it = 0;
+      int it = min(p.stages, slabs);
       for (; it < slabs; ++it) {
-        const int s = it % p.stages;
-        if (it >= p.stages &&
-            !mbar_wait(bar(C::kBarEmpty + s), (static_cast<uint32_t>(it / p.stages) & 1) ^ 1, abort_flag))
+        if (!mbar_wait(bar(C::kBarEmpty + it % p.stages), (static_cast<uint32_t>(it / p.stages) & 1) ^ 1, abort_flag))
           break;
-        mbar_arrive_expect_tx(bar(C::kBarFull + s), p.stage_bytes);
-        const uint32_t dst = base + s * p.stage_bytes;
-        tma_load_2d(dst, &p.tm_b, bar(C::kBarFull + s), (k0 + it) * 128, n0, pol_w);
-        tma_load_2d(dst + C::kWBytes, &p.tm_a, bar(C::kBarFull + s), (k0 + it) * 128, m0, pol_t);
+        load(it);
       }
       // let the copies still in flight land before the CTA can exit (matters only after an abort)
       for (int q = max(0, it - p.stages); q < it; ++q)
@@ -411,16 +425,30 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
       mbar_wait_drain(bar(C::kBarAccFull), 0);
     }
   } else {
-    // ---------------------------------------------------------------- sums to shared memory
-    // (the stages' memory: every MMA that reads it has retired)
-    if (warp_wait(bar(C::kBarAccFull), 0, abort_flag)) {
-      tc_fence_after();
-      int32_t* part = reinterpret_cast<int32_t*>(smem) + warp * 32 + lane;  // [T][128]
-      for (int t = 0; t < p.T; t += 16) {
-        uint32_t r[16];
-        tmem_ld16_wait(tmem + t + (static_cast<uint32_t>(warp * 32) << 16), r);
+    acc_ok = warp_wait(bar(C::kBarAccFull), 0, abort_flag);
+    tc_fence_after();
+  }
+  __syncwarp();
+  cluster_sync();  // every MMA of the cluster has read its stages: their memory takes the sums
+
+  // ------------------------------------------------------------------ sums to their owners
+  // Token t belongs to CTA t % splits, which gets [splits][per][128] sums.  Stores to the other
+  // CTAs, so that no warp waits for a remote load (each CTA reading its share from the others took
+  // 21.6 us at 256 x 5120 x 5120, this 18.3).
+  const int per = (p.T + splits - 1) / splits;
+  if (warp < 4 && acc_ok) {
+    int owner = 0, idx = 0;
+    const uint32_t mine = base + static_cast<uint32_t>(rank * per * 128 + warp * 32 + lane) * 4u;
+    for (int t = 0; t < p.T; t += 16) {
+      uint32_t r[16];
+      tmem_ld16_wait(tmem + t + (static_cast<uint32_t>(warp * 32) << 16), r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part[(t + i) * 128] = static_cast<int32_t>(r[i]);
+      for (int i = 0; i < 16; ++i) {
+        st_cluster_b32(cluster_map(mine + static_cast<uint32_t>(idx) * 512u, owner), r[i]);
+        if (++owner == splits) {
+          owner = 0;
+          ++idx;
+        }
       }
     }
   }
@@ -428,50 +456,121 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
   tc_fence_before();
   cluster_sync();
 
-  // ------------------------------------------------------------------ joined sums, scaled and stored
-  // A warp takes a token, a lane four channels; tokens go round the cluster and its warps.
-  if (warp < 4) {
-    const int n = n0 + 4 * lane;
-    float sb[4], bi[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sb[i] = n + i < p.N ? p.b_scale[n + i] : 0.f;
-      bi[i] = n + i < p.N && p.bias ? p.bias[n + i] : 0.f;
+  // ------------------------------------------------------------------ joined, scaled and stored
+  // a warp takes a token, a lane four channels
+  for (int idx = warp; rank + splits * idx < tokens; idx += C::kThreads / 32) {
+    const int m = m0 + rank + splits * idx;
+    if (idx != warp) sa = p.a_scale[m];
+    int4 v = make_int4(0, 0, 0, 0);
+    for (int c = 0; c < splits; ++c) {
+      const uint4 u = lds128(base + static_cast<uint32_t>((c * per + idx) * 512 + 16 * lane));
+      v.x += static_cast<int>(u.x);
+      v.y += static_cast<int>(u.y);
+      v.z += static_cast<int>(u.z);
+      v.w += static_cast<int>(u.w);
     }
-    const int tokens = min(p.T, p.M - m0);
-    for (int t = rank * 4 + warp; t < tokens; t += 4 * splits) {
-      const uint32_t at = base + static_cast<uint32_t>(t) * 512u + 16u * lane;
-      const float sa = p.a_scale[m0 + t];
-      int4 part[8];
+    const float f[4] = {scale_acc(v.x, sa, sb[0], bi[0]), scale_acc(v.y, sa, sb[1], bi[1]),
+                        scale_acc(v.z, sa, sb[2], bi[2]), scale_acc(v.w, sa, sb[3], bi[3])};
+    O* dst = static_cast<O*>(p.out) + m * p.o_stride + n;
+    if (p.vec && n + 4 <= p.N) {
+      if constexpr (sizeof(O) == 4) *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+      else *reinterpret_cast<uint2*>(dst) = make_uint2(pack_out2<O>(f[0], f[1]), pack_out2<O>(f[2], f[3]));
+    } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) part[c] = c < splits ? ld_cluster_v4(cluster_map(at, c)) : make_int4(0, 0, 0, 0);
-      int4 v = part[0];
-#pragma unroll
-      for (int c = 1; c < 8; ++c) {
-        v.x += part[c].x;
-        v.y += part[c].y;
-        v.z += part[c].z;
-        v.w += part[c].w;
-      }
-      const float f[4] = {scale_acc(v.x, sa, sb[0], bi[0]), scale_acc(v.y, sa, sb[1], bi[1]),
-                          scale_acc(v.z, sa, sb[2], bi[2]), scale_acc(v.w, sa, sb[3], bi[3])};
-      O* dst = static_cast<O*>(p.out) + (m0 + t) * p.o_stride + n;
-      if (p.vec && n + 4 <= p.N) {
-        if constexpr (sizeof(O) == 4) *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
-        else *reinterpret_cast<uint2*>(dst) = make_uint2(pack_out2<O>(f[0], f[1]), pack_out2<O>(f[2], f[3]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < p.N) dst[i] = from_f32<O>(f[i]);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (n + i < p.N) dst[i] = from_f32<O>(f[i]);
     }
   }
-  __syncwarp();
-  cluster_sync();  // this CTA's sums stay until every CTA of the cluster has read them
   if (warp == 5) {
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem_cols);
   }
+}
+
+// -------------------------------------------------------------------------------------
+// Up to 8 tokens: the weight straight from HBM into the registers of warp-level MMAs
+// -------------------------------------------------------------------------------------
+//
+// One token's product reads the weight once and does next to nothing else, and at its few
+// microseconds every hand-over counts (TMA descriptors, TMEM, clusters).  Here a CTA takes 16
+// channels and its warps every kWarps-th 64-byte piece of K.  The sum does not care for the order
+// of k, so a lane loads 16 neighbouring bytes of a row and takes them for the four words that
+// m16n8k32 wants at other places of k, with the tokens' bytes in the same order: no shared memory
+// and no shuffles before the warps' sums are joined.  (With a second tile of 8 tokens the registers
+// allow too few loads in flight: 11 us at 16 x 6144 x 4096, the split kernel 9.7.)
+
+struct MatmulRowsParams {
+  const int8_t* a;
+  const int8_t* b;
+  const float* a_scale;
+  const float* b_scale;
+  const float* bias;  // or nullptr
+  void* out;
+  int64_t a_stride, b_stride, o_stride;
+  int M, N, K;
+};
+
+__device__ __forceinline__ void mma_m16n8k32_s8(int32_t (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 bytes of a row from byte k on, zeros from K on.
+__device__ __forceinline__ uint4 load_codes16(const int8_t* row, int k, int K) {
+  if (k + 16 <= K) return ld_stream_v4(reinterpret_cast<const uint4*>(row + k));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 15; ++i)
+    if (k + i < K) w[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k + i])) << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename O, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32) matmul_i8_rows_kernel(const __grid_constant__ MatmulRowsParams p) {
+  constexpr int kUnroll = 4;
+  __shared__ int32_t part[kWarps][8][17];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+  const int n0 = blockIdx.x * 16;
+  // thread i of the first 16 M scales and stores token i / 16, channel i % 16 (8 x 16 <= 4 warps)
+  const int m = threadIdx.x >> 4, n = n0 + (threadIdx.x & 15);
+  const bool mine = m < p.M && n < p.N;
+  const float sa = mine ? p.a_scale[m] : 0.f, sb = mine ? p.b_scale[n] : 0.f, bias = mine && p.bias ? p.bias[n] : 0.f;
+  // rows past the end repeat the last one; their sums are not stored
+  const int8_t* w0 = p.b + min(n0 + g, p.N - 1) * p.b_stride;
+  const int8_t* w1 = p.b + min(n0 + g + 8, p.N - 1) * p.b_stride;
+  const int8_t* token = p.a + min(g, p.M - 1) * p.a_stride;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  int32_t acc[4] = {};
+  for (int k0 = warp * 64; k0 < p.K; k0 += kUnroll * kWarps * 64) {
+    uint4 a0[kUnroll], a1[kUnroll], x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int k = k0 + u * kWarps * 64 + tig * 16;
+      const bool in = k < p.K;
+      a0[u] = in ? load_codes16(w0, k, p.K) : zero;
+      a1[u] = in ? load_codes16(w1, k, p.K) : zero;
+      x[u] = in && g < p.M ? load_codes16(token, k, p.K) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      mma_m16n8k32_s8(acc, a0[u].x, a1[u].x, a0[u].y, a1[u].y, x[u].x, x[u].y);
+      mma_m16n8k32_s8(acc, a0[u].z, a1[u].z, a0[u].w, a1[u].w, x[u].z, x[u].w);
+    }
+  }
+  // lane (g, tig) holds channels g, g + 8 of tokens 2 tig, 2 tig + 1
+  part[warp][2 * tig][g] = acc[0];
+  part[warp][2 * tig + 1][g] = acc[1];
+  part[warp][2 * tig][g + 8] = acc[2];
+  part[warp][2 * tig + 1][g + 8] = acc[3];
+  __syncthreads();
+  if (!mine) return;
+  int32_t sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) sum += part[w][m][threadIdx.x & 15];
+  static_cast<O*>(p.out)[m * p.o_stride + n] = from_f32<O>(scale_acc(sum, sa, sb, bias));
 }
 
 }  // namespace qbsa

@@ -915,8 +915,20 @@ qbsa_status matmul_i8_split(const MatmulArgs& g, int sms, cudaStream_t s) {
   const int per_sm = prm.T <= 64 ? 2 : 1;
   const int room = 232448 / per_sm - (per_sm > 1 ? 1024 : 0) - 1024 - C::kTailBytes;  // 1 KB a CTA is the system's
   prm.stages = std::min(C::kMaxStages, room / prm.stage_bytes);
+  // CTAs of a tile (the cluster): as few rounds of resident CTAs, and slabs per round, as there can
+  // be; a round's fixed cost is about six slabs.  Clusters of more than two leave some SMs of a
+  // graphics cluster unused (an eighth covers sizes up to 6; 7 and 8 fit worse).
   const int64_t tiles = (int64_t)tiles_m * tiles_n;
-  int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, (int64_t)sms * per_sm / tiles, prm.slabs})));
+  int splits = 1;
+  int64_t best = INT64_MAX;
+  for (int c = 1; c <= std::min(6, prm.slabs); ++c) {
+    const int64_t room = std::max(1, (c <= 2 ? sms : sms * 7 / 8) * per_sm / c);
+    const int64_t cost = (tiles + room - 1) / room * ((prm.slabs + c - 1) / c + 6);
+    if (cost < best) {
+      best = cost;
+      splits = c;
+    }
+  }
   prm.slabs_per = (prm.slabs + splits - 1) / splits;
   splits = (prm.slabs + prm.slabs_per - 1) / prm.slabs_per;
   prm.tmem_cols = 32;
@@ -955,10 +967,21 @@ qbsa_status matmul_i8_split(const MatmulArgs& g, int sms, cudaStream_t s) {
 }
 
 template <typename O>
+qbsa_status matmul_i8_rows(const MatmulArgs& g, int sms, cudaStream_t s) {
+  const qbsa::MatmulRowsParams prm = {g.a,  g.b,        g.a_scale,  g.b_scale,  g.bias, g.out,
+                                      g.a_stride, g.b_stride, g.o_stride, g.M, g.N, g.K};
+  const unsigned grid = (g.N + 15) / 16;
+  if (grid <= static_cast<unsigned>(sms)) qbsa::matmul_i8_rows_kernel<O, 16><<<grid, 512, 0, s>>>(prm);
+  else qbsa::matmul_i8_rows_kernel<O, 8><<<grid, 256, 0, s>>>(prm);
+  return check_launch("matmul_i8_rows_kernel launch");
+}
+
+template <typename O>
 qbsa_status matmul_i8_launch(const MatmulArgs& g, cudaStream_t s) {
   int sms = 0;
   const qbsa_status st = sm_count(&sms);
   if (st != QBSA_OK) return st;
+  if (g.M <= 8) return matmul_i8_rows<O>(g, sms, s);
   return g.M <= 256 ? matmul_i8_split<O>(g, sms, s) : matmul_i8_pair<O>(g, sms, s);
 }
 
