@@ -31,91 +31,95 @@ __device__ __forceinline__ uint32_t pack_out2(float lo, float hi) {
 }
 
 // -------------------------------------------------------------------------------------
-// Many tokens: a pair of CTAs per 256 x BN tile
+// Many tokens: a pair of CTAs per 256 x W tile
 // -------------------------------------------------------------------------------------
 //
 // Two CTAs of a cluster share one tile (tcgen05 cta_group::2): each holds 128 of its 256 token
-// rows and half of its BN channels in shared memory, and the tensor cores of both read both
+// rows and half of its W <= 256 channels in shared memory, and the tensor cores of both read both
 // halves, so a byte of B fetched once serves 256 rows.  The grid stays resident and each pair
-// walks the tiles; sums alternate between two TMEM buffers, so that one tile is scaled and
+// walks the tiles; sums alternate between two TMEM accumulators, so that one tile is scaled and
 // stored while the next is multiplied.
 //
-// CTA = 8 warps: 0 TMA producer (A rows and B rows of this CTA; the bytes of both CTAs complete
-// on the even CTA's barrier), 1 MMA issuer (even CTA only), 2 TMEM owner, 4-7 epilogue, one
-// TMEM lane quarter each: scale, round, stage 32 rows x 128 bytes, TMA store.
+// An MMA of 256 x N x 32 takes 128 cycles at N = 256, but 113 at 192 and 107 at 128 (timed without
+// the loads), so narrow tiles are for small products only.  A tile of 512 channels in both
+// accumulators, with a quarter fewer bytes from L2, lost more where the accumulators change hands
+// than it gained (568 us against 546 at 32768 x 5120 x 5120).
+//
+// CTA = 8 or 12 warps: 0 TMA producer (A rows and B rows of this CTA; the bytes of both CTAs
+// complete on the even CTA's barrier), 1 MMA issuer (even CTA only), 2 TMEM owner, 4 and up
+// epilogue, one or two per TMEM lane quarter: scale, round, turn 32 rows x 128 bytes through shared
+// memory, store whole lines.  kEpi = 8 takes a stage of the ring from kEpi = 4 (long K: KPLACE).
 
 struct MatmulPairParams {
   CUtensorMap tm_a;    // {K, M} bytes, box {128, 128}, SW128
-  CUtensorMap tm_b;    // {K, N} bytes, box {128, BN / 2}, SW128
-  CUtensorMap tm_out;  // {N, M}, box {128 bytes, 32}, SW128 (out_tma)
+  CUtensorMap tm_b;    // {K, N} bytes, box {128, W / 2}, SW128
   const float* a_scale;
   const float* b_scale;
   const float* bias;  // or nullptr
   void* out;
   int64_t o_stride;
   int M, N, slabs;  // slabs of 128 bytes of K
-  int BN;
+  int W;
   int tiles_m, tiles_n;
-  int out_tma;  // rows of out on 16-byte boundaries
+  int stages, stage_bytes;
+  int out_vec;  // rows of out on 16-byte boundaries
 };
 
+template <int kEpi>  // epilogue warps
 struct MatmulPairCfg {
-  static constexpr int kThreads = 256;
-  static constexpr int kStages = 6;
+  static constexpr int kThreads = 128 + 32 * kEpi;
+  static constexpr int kMaxStages = 8;
   static constexpr int kABytes = 128 * 128;
-  static constexpr int kStageBytes = 2 * kABytes;  // B: at most 128 rows
-  static constexpr int kOutOff = kStages * kStageBytes;
+  static constexpr int kRingBytes = (kEpi == 4 ? 6 : 5) * 2 * kABytes;
+  static constexpr int kOutOff = kRingBytes;
   static constexpr int kOutBytes = 32 * 128;  // per epilogue warp
-  static constexpr int kColOff = kOutOff + 4 * kOutBytes;
+  static constexpr int kColOff = kOutOff + kEpi * kOutBytes;
   static constexpr int kColBytes = 2 * 256 * 4;  // b_scale and bias of a tile, per epilogue warp
-  static constexpr int kBarOff = kColOff + 4 * kColBytes;
+  static constexpr int kBarOff = kColOff + kEpi * kColBytes;
   static constexpr int kBarFull = 0;
-  static constexpr int kBarEmpty = kBarFull + kStages;
-  static constexpr int kBarAccFull = kBarEmpty + kStages;
+  static constexpr int kBarEmpty = kBarFull + kMaxStages;
+  static constexpr int kBarAccFull = kBarEmpty + kMaxStages;
   static constexpr int kBarAccEmpty = kBarAccFull + 2;
   static constexpr int kBarDrain = kBarAccEmpty + 2;
   static constexpr int kNumBars = kBarDrain + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
   static constexpr int kGroupM = 8;  // tile rows walked together, for L2
+  static_assert(kSmemBytes <= 232448, "shared memory above the 227 KB opt-in limit");
 };
-static_assert(MatmulPairCfg::kSmemBytes <= 232448, "shared memory above the 227 KB opt-in limit");
 
-// 32 rows x 128 bytes of scaled sums: from `acc` (this lane's row) to the staging tile, swizzled
-// as the output's tensor map reads it.  col: b_scale and, 256 further on, bias of the columns.
+// 128 bytes of scaled and rounded sums from `acc` (this lane's row).  col: b_scale and, 256 further
+// on, bias of the columns.
 template <typename O, int kCols>
-__device__ __forceinline__ void stage_out(uint32_t stage, int lane, const uint32_t (&acc)[kCols], float sa,
-                                          const float* col) {
-  constexpr int kPer = 16 / sizeof(O);  // values of 16 bytes
+__device__ __forceinline__ void round_out(uint32_t (&w)[32], const uint32_t (&acc)[kCols], float sa, const float* col) {
+  const float2 sa2 = make_float2(sa, sa);
 #pragma unroll
-  for (int x = 0; x < 8; ++x) {
-    float f[kPer];
+  for (int x = 0; x < kCols; x += 4) {
+    const float4 sb = *reinterpret_cast<const float4*>(col + x);
+    const float4 bi = *reinterpret_cast<const float4*>(col + 256 + x);
+    float2 f[2];  // scale_acc, two at a time
 #pragma unroll
-    for (int y = 0; y < kPer; y += 4) {
-      const float4 sb = *reinterpret_cast<const float4*>(col + x * kPer + y);
-      const float4 bi = *reinterpret_cast<const float4*>(col + 256 + x * kPer + y);
-      const uint32_t* v = acc + x * kPer + y;
-      f[y] = scale_acc(v[0], sa, sb.x, bi.x);
-      f[y + 1] = scale_acc(v[1], sa, sb.y, bi.y);
-      f[y + 2] = scale_acc(v[2], sa, sb.z, bi.z);
-      f[y + 3] = scale_acc(v[3], sa, sb.w, bi.w);
+    for (int y = 0; y < 2; ++y) {
+      f[y] = make_float2(__int2float_rn(static_cast<int32_t>(acc[x + 2 * y])),
+                         __int2float_rn(static_cast<int32_t>(acc[x + 2 * y + 1])));
+      f[y] = mul2(f[y], sa2);
     }
-    uint32_t w[4];
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      if constexpr (sizeof(O) == 4) w[y] = __float_as_uint(f[y]);
-      else w[y] = pack_out2<O>(f[2 * y], f[2 * y + 1]);
+    f[0] = fma2(f[0], make_float2(sb.x, sb.y), make_float2(bi.x, bi.y));
+    f[1] = fma2(f[1], make_float2(sb.z, sb.w), make_float2(bi.z, bi.w));
+    if constexpr (sizeof(O) == 4) {
+      w[x] = __float_as_uint(f[0].x), w[x + 1] = __float_as_uint(f[0].y);
+      w[x + 2] = __float_as_uint(f[1].x), w[x + 3] = __float_as_uint(f[1].y);
+    } else {
+      w[x / 2] = pack2<O>(f[0]);
+      w[x / 2 + 1] = pack2<O>(f[1]);
     }
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((x ^ (lane & 7)) << 4)),
-                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                 : "memory");
   }
 }
 
-template <typename O>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MatmulPairCfg::kThreads, 1)
+template <typename O, int kEpi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MatmulPairCfg<kEpi>::kThreads, 1)
     matmul_i8_pair_kernel(const __grid_constant__ MatmulPairParams p) {
-  using C = MatmulPairCfg;
+  using C = MatmulPairCfg<kEpi>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;
@@ -129,19 +133,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MatmulPairCfg::kThre
   if (warp == 0) {
     if (lane == 0) {
       *abort_flag = 0;
-      for (int s = 0; s < C::kStages; ++s) {
+      for (int s = 0; s < p.stages; ++s) {
         mbar_init(bar(C::kBarFull + s), 1);
         mbar_init(bar(C::kBarEmpty + s), 1);
       }
       for (int t = 0; t < 2; ++t) {
         mbar_init(bar(C::kBarAccFull + t), 1);
-        mbar_init(bar(C::kBarAccEmpty + t), 8);  // the epilogue warps of both CTAs
+        mbar_init(bar(C::kBarAccEmpty + t), 2 * kEpi);  // the epilogue warps of both CTAs
       }
       mbar_init(bar(C::kBarDrain), 1);
       fence_mbar_init();
       tma_prefetch_desc(&p.tm_a);
       tma_prefetch_desc(&p.tm_b);
-      if (p.out_tma) tma_prefetch_desc(&p.tm_out);
     }
   } else if (warp == 2) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
@@ -161,63 +164,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MatmulPairCfg::kThre
     const int g = t / per_group, r = t - g * per_group;
     const int rows = min(C::kGroupM, p.tiles_m - g * C::kGroupM);
     m0 = (g * C::kGroupM + r % rows) * 256;
-    n0 = r / rows * p.BN;
+    n0 = r / rows * p.W;
   };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
     if (lane == 0) {
       const uint32_t full0 = cluster_map(bar(C::kBarFull), 0);  // the even CTA's barriers
-      const uint32_t bytes = 2u * (C::kABytes + static_cast<uint32_t>(p.BN / 2) * 128u);
       const uint64_t pol_a = l2_policy_evict_first(), pol_b = l2_policy_evict_last();
-      int it = 0;
+      const uint32_t bytes = 2u * static_cast<uint32_t>(p.stage_bytes);
+      const int slabs = p.slabs, stages = p.stages;
+      int it = 0, s = 0;
+      uint32_t phase = 1;  // parity of the phase that a stage's reader completed last: none yet
+      uint32_t dst = base, full = full0, own = bar(C::kBarFull);
+      constexpr uint32_t kToEmpty = 8u * (C::kBarEmpty - C::kBarFull);
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += pairs) {
         int m0, n0;
         tile_at(t, m0, n0);
-        for (int k = 0; k < p.slabs; ++k, ++it) {
-          const int s = it % C::kStages;
-          if (it >= C::kStages &&
-              !mbar_wait<true>(bar(C::kBarEmpty + s), (static_cast<uint32_t>(it / C::kStages) & 1) ^ 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(bar(C::kBarFull + s), bytes);
-          const uint32_t dst = base + s * C::kStageBytes, full = full0 + 8u * s;
-          tma_load_2d_pair(dst, &p.tm_a, full, k * 128, m0 + static_cast<int>(rank) * 128, pol_a);
-          tma_load_2d_pair(dst + C::kABytes, &p.tm_b, full, k * 128, n0 + static_cast<int>(rank) * (p.BN / 2), pol_b);
+        m0 += static_cast<int>(rank) * 128;
+        n0 += static_cast<int>(rank) * (p.W / 2);
+#pragma unroll 2
+        for (int k = 0; k < slabs; ++k, ++it) {
+          if (!(ok = mbar_wait_hot(own + kToEmpty, phase, abort_flag))) break;
+          if (rank == 0) mbar_arrive_expect_tx(own, bytes);
+          tma_load_2d_pair(dst, &p.tm_a, full, k * 128, m0, pol_a);
+          tma_load_2d_pair(dst + C::kABytes, &p.tm_b, full, k * 128, n0, pol_b);
+          const bool wrap = ++s == stages;
+          s = wrap ? 0 : s;
+          phase ^= wrap ? 1u : 0u;
+          dst = wrap ? base : dst + p.stage_bytes;
+          full = wrap ? full0 : full + 8u;
+          own = wrap ? bar(C::kBarFull) : own + 8u;
         }
       }
       // let the copies still in flight land before the pair can exit (matters only after an
       // abort): the even CTA's barriers count the bytes of both
       if (rank == 0)
-        for (int q = max(0, it - C::kStages); q < it; ++q)
-          mbar_wait_drain(bar(C::kBarFull + q % C::kStages), static_cast<uint32_t>(q / C::kStages) & 1);
+        for (int q = max(0, it - p.stages); q < it; ++q)
+          mbar_wait_drain(bar(C::kBarFull + q % p.stages), static_cast<uint32_t>(q / p.stages) & 1);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_s8(256, p.BN);
-      int it = 0, n = 0;
+      // One thread issues everything, each instruction some cycles after the one before it, so what
+      // it does per slab is kept short: stage addresses and descriptors are stepped, not computed
+      // (with the address arithmetic in the loop a slab took 850 cycles at any width).
+      const uint32_t idesc = idesc_s8(256, p.W);
+      const uint64_t desc0 = sdesc_sw128(base, 16, 1024);
+      const uint32_t desc_hi = static_cast<uint32_t>(desc0 >> 32), desc_lo0 = static_cast<uint32_t>(desc0);
+      const uint32_t step = static_cast<uint32_t>(p.stage_bytes) >> 4;
+      constexpr uint32_t b_off = C::kABytes >> 4;
+      const uint32_t full_0 = bar(C::kBarFull), full_end = bar(C::kBarFull + p.stages);
+      constexpr uint32_t kToEmpty = 8u * (C::kBarEmpty - C::kBarFull);
+      const int slabs = p.slabs;
+      struct Stage {
+        uint32_t full, desc, phase;  // its full barrier, lower descriptor word and parity
+      } st = {full_0, desc_lo0, 0u};
+      auto advance = [&](Stage& x) {
+        const bool wrap = x.full + 8u == full_end;
+        x.full = wrap ? full_0 : x.full + 8u;
+        x.desc = wrap ? desc_lo0 : x.desc + step;
+        x.phase ^= wrap ? 1u : 0u;
+      };
       bool ok = true;
-      for (int t = pair; ok && t < tiles; t += pairs, ++n) {
-        const int acc = n & 1;
-        if (n >= 2 && !mbar_wait<true>(bar(C::kBarAccEmpty + acc), (static_cast<uint32_t>(n / 2) & 1) ^ 1, abort_flag))
+      int unit = 0;  // tiles begun
+      for (int t = pair; ok && t < tiles; t += pairs, ++unit) {
+        const int acc = unit & 1;
+        if (unit >= 2 &&
+            !mbar_wait_hot<true>(bar(C::kBarAccEmpty + acc), (static_cast<uint32_t>(unit / 2) & 1) ^ 1, abort_flag))
           break;
         tc_fence_after();
-        for (int k = 0; k < p.slabs; ++k, ++it) {
-          const int s = it % C::kStages;
-          if (!mbar_wait<true>(bar(C::kBarFull + s), static_cast<uint32_t>(it / C::kStages) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
+        const uint32_t d = tmem + acc * 256;
+#pragma unroll 4
+        for (int k = 0; k < slabs; ++k) {
+          if (!(ok = mbar_wait_hot(st.full, st.phase, abort_flag))) break;
           tc_fence_after();
-          const uint32_t a = base + s * C::kStageBytes, b = a + C::kABytes;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_i8_ss_pair(tmem + acc * 256, sdesc_sw128(a + kk * 32, 16, 1024), sdesc_sw128(b + kk * 32, 16, 1024),
-                           idesc, (k | kk) != 0 ? 1u : 0u);
-          mma_commit_pair(bar(C::kBarEmpty + s));
+          mma_i8_ss_pair_x4(d, st.desc, st.desc + b_off, desc_hi, idesc, static_cast<uint32_t>(k));
+          mma_commit_pair(st.full + kToEmpty);
+          advance(st);
         }
         if (ok) mma_commit_pair(bar(C::kBarAccFull + acc));
       }
@@ -229,65 +254,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MatmulPairCfg::kThre
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     constexpr int kCols = 128 / sizeof(O);  // columns of a staged piece
-    const int quarter = warp & 3;
-    const uint32_t stage = base + C::kOutOff + quarter * C::kOutBytes;
-    float* col = reinterpret_cast<float*>(smem + C::kColOff + quarter * C::kColBytes);
+    constexpr int kTurns = kEpi / 4;            // the warps of a quarter take a tile's pieces in turn
+    const int quarter = warp & 3, own = warp - 4, first = own / 4 * kCols;
+    const uint32_t stage = base + C::kOutOff + own * C::kOutBytes;
+    float* col = reinterpret_cast<float*>(smem + C::kColOff + own * C::kColBytes);
     const uint32_t empty0 = cluster_map(bar(C::kBarAccEmpty), 0);
-    int n = 0;
-    for (int t = pair; t < tiles; t += pairs, ++n) {
+    // b_scale and bias of a tile's channels, a_scale of this lane's row: the next tile's are on
+    // their way while a tile is stored
+    float sb[8], bi[8], sa_next = 0.f;
+    auto prefetch = [&](int t) {
       int m0, n0;
       tile_at(t, m0, n0);
-      const int acc = n & 1;
-      const int m_warp = m0 + static_cast<int>(rank) * 128 + quarter * 32, m = m_warp + lane;
-      for (int c = lane; c < p.BN; c += 32) {
-        const bool in = n0 + c < p.N;
-        col[c] = in ? p.b_scale[n0 + c] : 0.f;
-        col[256 + c] = in && p.bias ? p.bias[n0 + c] : 0.f;
+      const int m = m0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+      sa_next = m < p.M ? p.a_scale[m] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = 32 * i + lane, n = n0 + c;
+        const bool in = c < p.W && n < p.N;
+        sb[i] = in ? p.b_scale[n] : 0.f;
+        bi[i] = in && p.bias ? p.bias[n] : 0.f;
       }
-      const float sa = m < p.M ? p.a_scale[m] : 0.f;
+    };
+    if (pair < tiles) prefetch(pair);
+    int unit = 0;
+    for (int t = pair; t < tiles; t += pairs, ++unit) {
+      int m0, n0;
+      tile_at(t, m0, n0);
+      const int m_warp = m0 + static_cast<int>(rank) * 128 + quarter * 32;
+      const float sa = sa_next;
+      const int acc = unit & 1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        col[32 * i + lane] = sb[i];
+        col[256 + 32 * i + lane] = bi[i];
+      }
       __syncwarp();
-      if (!warp_wait(bar(C::kBarAccFull + acc), static_cast<uint32_t>(n / 2) & 1, abort_flag)) break;
+      if (t + pairs < tiles) prefetch(t + pairs);
+      const bool ok =
+          lane != 0 || mbar_wait_hot(bar(C::kBarAccFull + acc), static_cast<uint32_t>(unit / 2) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t src = tmem + acc * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
-      for (int c = 0; c < p.BN; c += kCols) {
-        uint32_t r[kCols];
+      for (int c = first; c < p.W; c += kTurns * kCols) {
+        uint32_t r[kCols], w[32];
         if constexpr (kCols == 64) tmem_ld64_wait(src + c, r);
         else tmem_ld32_wait(src + c, r);
-        if (c + kCols >= p.BN) {  // the sums are out of TMEM: the next tile but one may have it
+        if (c + kTurns * kCols >= p.W) {  // this warp's sums are out of TMEM: the next tile but one may have it
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(empty0 + 8u * acc);
         }
         if (m_warp >= p.M || n0 + c >= p.N) continue;
-        if (lane == 0) bulk_wait_read_all();  // the staging tile's previous store
-        __syncwarp();
-        stage_out<O, kCols>(stage, lane, r, sa, col + c);
-        if (p.out_tma) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&p.tm_out, stage, n0 + c, m_warp);
-            bulk_commit_group();
-          }
-        } else {
-          // rows of out at any alignment: a warp writes a row's piece at a time
-          __syncwarp();
-          const int rows = min(32, p.M - m_warp), cols = min(kCols, p.N - n0 - c);
-          for (int i = 0; i < rows; ++i) {
-            O* dst = static_cast<O*>(p.out) + (m_warp + i) * p.o_stride + n0 + c;
+        round_out<O, kCols>(w, r, sa, col + c);
+        // 16-byte chunk x of row r lies at chunk x ^ (r % 8): conflict-free both ways
 #pragma unroll
-            for (int j = lane; j < kCols; j += 32) {
-              const int at = j * static_cast<int>(sizeof(O));
-              if (j < cols)
-                dst[j] = *reinterpret_cast<const O*>(smem + C::kOutOff + quarter * C::kOutBytes + i * 128 +
-                                                     (((at >> 4) ^ (i & 7)) << 4) + (at & 15));
+        for (int x = 0; x < 8; ++x)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((x ^ (lane & 7)) << 4)),
+                       "r"(w[4 * x]), "r"(w[4 * x + 1]), "r"(w[4 * x + 2]), "r"(w[4 * x + 3])
+                       : "memory");
+        __syncwarp();
+        const int rows = min(32, p.M - m_warp), cols = min(kCols, p.N - n0 - c);
+        O* const dst = static_cast<O*>(p.out) + m_warp * p.o_stride + n0 + c;
+        if (p.out_vec && cols == kCols) {
+          const int x = lane & 7;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3);
+            const uint4 v = lds128(stage + row * 128 + ((x ^ (row & 7)) << 4));
+            if (row < rows)
+              *reinterpret_cast<uint4*>(dst + row * p.o_stride + x * (16 / static_cast<int>(sizeof(O)))) = v;
+          }
+        } else {  // rows at any alignment, or the last columns
+          const uint8_t* const staged = smem + C::kOutOff + own * C::kOutBytes;
+#pragma unroll 8
+          for (int i = 0; i < 32; ++i) {
+#pragma unroll
+            for (int j = 0; j < kCols; j += 32) {
+              const int at = (j + lane) * static_cast<int>(sizeof(O));
+              const O v = *reinterpret_cast<const O*>(staged + i * 128 + (((at >> 4) ^ (i & 7)) << 4) + (at & 15));
+              if (i < rows && j + lane < cols) dst[i * p.o_stride + j + lane] = v;
             }
           }
-          __syncwarp();
         }
+        __syncwarp();
       }
+      if (first >= p.W) {  // a narrow tile: no piece for this warp
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(empty0 + 8u * acc);
+      }
+      __syncwarp();  // col is read
     }
-    if (lane == 0) bulk_wait_read_all();  // shared memory must outlive the stores' reads
   }
 
   __syncwarp();
@@ -397,7 +454,7 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
     if (lane == 0) {
       int it = min(p.stages, slabs);
       for (; it < slabs; ++it) {
-        if (!mbar_wait(bar(C::kBarEmpty + it % p.stages), (static_cast<uint32_t>(it / p.stages) & 1) ^ 1, abort_flag))
+        if (!mbar_wait_hot(bar(C::kBarEmpty + it % p.stages), (static_cast<uint32_t>(it / p.stages) & 1) ^ 1, abort_flag))
           break;
         load(it);
       }
@@ -411,7 +468,7 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
       const uint32_t idesc = idesc_s8(128, p.T);
       for (int it = 0; it < slabs; ++it) {
         const int s = it % p.stages;
-        if (!mbar_wait(bar(C::kBarFull + s), static_cast<uint32_t>(it / p.stages) & 1, abort_flag)) break;
+        if (!mbar_wait_hot(bar(C::kBarFull + s), static_cast<uint32_t>(it / p.stages) & 1, abort_flag)) break;
         tc_fence_after();
         const uint32_t w = base + s * p.stage_bytes, x = w + C::kWBytes;
 #pragma unroll
@@ -425,7 +482,8 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
       mbar_wait_drain(bar(C::kBarAccFull), 0);
     }
   } else {
-    acc_ok = warp_wait(bar(C::kBarAccFull), 0, abort_flag);
+    acc_ok = lane != 0 || mbar_wait_hot(bar(C::kBarAccFull), 0, abort_flag);
+    acc_ok = __all_sync(0xffffffffu, acc_ok);
     tc_fence_after();
   }
   __syncwarp();

@@ -66,28 +66,13 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// The same for a barrier that other CTAs of the cluster arrive on.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Wait until the phase with the given parity has completed.  Returns false (and
 // raises *abort) if the CTA aborted or the wait exceeded the time limit.
-template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  const auto done = [&] { return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-  if (done()) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 1;; ++it) {
-    if (done()) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 0) {
       if (*abort) return false;
       if (global_timer_ns() - t0 > QBSA_WAIT_TIMEOUT_NS) {
@@ -97,6 +82,51 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
       }
     }
   }
+}
+
+// The same for the threads that hand the stages of a ring to each other: one instruction in the
+// common case (the thread is suspended until the phase completes, for up to 1 ms), and the rest out
+// of line.  A lone thread pays some twenty cycles for each branch that it takes, so that with the
+// loop above in line a slab of a product took 390 ns instead of 340, and with short polls 410.
+// kCluster: the barrier is one that threads of other CTAs arrive on.
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (kCluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+  return ok != 0;
+}
+template <bool kCluster>
+__device__ __noinline__ bool mbar_wait_rest(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait_long<kCluster>(bar, parity)) {
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > QBSA_WAIT_TIMEOUT_NS) {
+      *abort = 1;
+      atomicCAS(&g_device_error, 0u, static_cast<unsigned int>(kErrTimeout));
+      return false;
+    }
+  }
+  return true;
+}
+template <bool kCluster = false>
+__device__ __forceinline__ bool mbar_wait_hot(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (__builtin_expect(mbar_try_wait_long<kCluster>(bar, parity), 1)) return true;
+  return mbar_wait_rest<kCluster>(bar, parity, abort);
 }
 
 // ---------------------------------------------------------------------------------
@@ -218,14 +248,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, 
       : "memory");
 }
 
-// 2-D tiled TMA store from shared memory (bulk-group completion).  Rows and columns past the
-// tensor's extent are not written.
-__device__ __forceinline__ void tma_store_2d(const void* map, uint32_t src, int c0, int c1) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(src),
-               "r"(c0), "r"(c1)
-               : "memory");
-}
-
 // Tiled TMA store from shared memory (bulk-group completion; no multicast).  Rows
 // past the tensor's extent are not written.
 __device__ __forceinline__ void tma_store_4d(const void* map, uint32_t src, int c0, int c1, int c2, int c3) {
@@ -323,11 +345,22 @@ __device__ __forceinline__ void tmem_relinquish_pair() {
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-__device__ __forceinline__ void mma_i8_ss_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Four MMAs over 128 bytes of K (32 bytes, 2 descriptor units, each); the operands' descriptors
+// share their upper words, and their lower words start with the address.
+__device__ __forceinline__ void mma_i8_ss_pair_x4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                                  uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, one;\n\t.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n\t.reg .b32 x, y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 one, %3, %3;\n\t"
+      "mov.b64 a0, {%1, %3};\n\tmov.b64 b0, {%2, %3};\n\t"
+      "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a1, {x, %3};\n\tmov.b64 b1, {y, %3};\n\t"
+      "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 a2, {x, %3};\n\tmov.b64 b2, {y, %3};\n\t"
+      "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a3, {x, %3};\n\tmov.b64 b3, {y, %3};\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], a0, b0, %4, p;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], a1, b1, %4, one;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], a2, b2, %4, one;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], a3, b3, %4, one;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 // Arrive on the mbarrier at this address in both CTAs of the pair.

@@ -9,7 +9,6 @@
 #include <mutex>
 #include <numeric>
 #include <string>
-#include <type_traits>
 #include <vector>
 
 #include <cuda.h>
@@ -851,31 +850,28 @@ struct MatmulArgs {
   int M, N, K;
 };
 
-template <typename O>
-constexpr CUtensorMapDataType map_type() {
-  return sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                        : std::is_same<O, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-}
-
-template <typename O>
+template <typename O, int kEpi>
 qbsa_status matmul_i8_pair(const MatmulArgs& g, int sms, cudaStream_t s) {
-  using C = qbsa::MatmulPairCfg;
+  using C = qbsa::MatmulPairCfg<kEpi>;
   qbsa::MatmulPairParams prm;
   memset(&prm, 0, sizeof(prm));
   const int pairs = std::max(1, sms / 2);
   prm.tiles_m = (g.M + 255) / 256;
+  prm.slabs = (g.K + 127) / 128;
+  // Tile width: rounds of resident pairs, each of `slabs` slabs at the MMA's time for that width (four
+  // of 107 cycles at 128 channels and 128 at 256), and a fixed cost for filling and draining.
   int64_t best = INT64_MAX;
-  for (int bn = 256; bn >= 64; bn -= 32) {
-    if (128 % sizeof(O) != 0 || bn % (128 / sizeof(O)) != 0) continue;
-    const int64_t tiles = (int64_t)prm.tiles_m * ((g.N + bn - 1) / bn);
-    const int64_t cost = (tiles + pairs - 1) / pairs * (bn + 48);
+  for (int w = 256; w >= 64; w -= 64) {
+    const int64_t tiles = (int64_t)prm.tiles_m * ((g.N + w - 1) / w);
+    const int64_t cost = (tiles + pairs - 1) / pairs * (prm.slabs * (344 + w * 21 / 32) + 1500);
     if (cost < best) {
       best = cost;
-      prm.BN = bn;
+      prm.W = w;
     }
   }
-  prm.tiles_n = (g.N + prm.BN - 1) / prm.BN;
+  prm.tiles_n = (g.N + prm.W - 1) / prm.W;
+  prm.stage_bytes = C::kABytes + prm.W / 2 * 128;
+  prm.stages = std::min(C::kMaxStages, C::kRingBytes / prm.stage_bytes);
   prm.a_scale = g.a_scale;
   prm.b_scale = g.b_scale;
   prm.bias = g.bias;
@@ -883,22 +879,18 @@ qbsa_status matmul_i8_pair(const MatmulArgs& g, int sms, cudaStream_t s) {
   prm.o_stride = g.o_stride;
   prm.M = g.M;
   prm.N = g.N;
-  prm.slabs = (g.K + 127) / 128;
   qbsa_status st;
   if ((st = make_map_2d(&prm.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.K, g.M, g.a_stride, 128, 128)) != QBSA_OK)
     return st;
-  if ((st = make_map_2d(&prm.tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b, g.K, g.N, g.b_stride, 128, prm.BN / 2)) != QBSA_OK)
+  if ((st = make_map_2d(&prm.tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b, g.K, g.N, g.b_stride, 128, prm.W / 2)) != QBSA_OK)
     return st;
   const uint64_t pitch = g.o_stride * sizeof(O);
-  prm.out_tma = aligned16(g.out) && pitch % 16 == 0;
-  if (prm.out_tma &&
-      (st = make_map_2d(&prm.tm_out, map_type<O>(), g.out, g.N, g.M, pitch, 128 / sizeof(O), 32)) != QBSA_OK)
-    return st;
+  prm.out_vec = aligned16(g.out) && pitch % 16 == 0;
   static std::atomic<uint64_t> done{0};
-  if ((st = set_smem_once(qbsa::matmul_i8_pair_kernel<O>, C::kSmemBytes, done)) != QBSA_OK) return st;
+  if ((st = set_smem_once(qbsa::matmul_i8_pair_kernel<O, kEpi>, C::kSmemBytes, done)) != QBSA_OK) return st;
   const int64_t tiles = (int64_t)prm.tiles_m * prm.tiles_n;
   const unsigned grid = 2u * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
-  qbsa::matmul_i8_pair_kernel<O><<<grid, C::kThreads, C::kSmemBytes, s>>>(prm);
+  qbsa::matmul_i8_pair_kernel<O, kEpi><<<grid, C::kThreads, C::kSmemBytes, s>>>(prm);
   return check_launch("matmul_i8_pair_kernel launch");
 }
 
@@ -982,7 +974,8 @@ qbsa_status matmul_i8_launch(const MatmulArgs& g, cudaStream_t s) {
   const qbsa_status st = sm_count(&sms);
   if (st != QBSA_OK) return st;
   if (g.M <= 8) return matmul_i8_rows<O>(g, sms, s);
-  return g.M <= 256 ? matmul_i8_split<O>(g, sms, s) : matmul_i8_pair<O>(g, sms, s);
+  if (g.M <= 256) return matmul_i8_split<O>(g, sms, s);
+  return g.K <= 1024 ? matmul_i8_pair<O, 8>(g, sms, s) : matmul_i8_pair<O, 4>(g, sms, s);
 }
 
 // The checks and launch that qbsa_rms_norm_quant and qbsa_quantize_token share.
