@@ -48,7 +48,8 @@ __device__ __forceinline__ uint32_t pack_out2(float lo, float hi) {
 // CTA = 8 or 12 warps: 0 TMA producer (A rows and B rows of this CTA; the bytes of both CTAs
 // complete on the even CTA's barrier), 1 MMA issuer (even CTA only), 2 TMEM owner, 4 and up
 // epilogue, one or two per TMEM lane quarter: scale, round, turn 32 rows x 128 bytes through shared
-// memory, store whole lines.  kEpi = 8 takes a stage of the ring from kEpi = 4 (long K: KPLACE).
+// memory, store whole lines.  kEpi = 8 takes a stage of the ring from kEpi = 4
+// (4096 x 6144 x 4096: 70.4 us with six stages, 74.5 with five).
 
 struct MatmulPairParams {
   CUtensorMap tm_a;    // {K, M} bytes, box {128, 128}, SW128

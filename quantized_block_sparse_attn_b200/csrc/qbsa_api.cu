@@ -850,26 +850,59 @@ struct MatmulArgs {
   int M, N, K;
 };
 
+// How a product would be cut for the two tensor-core kernels, and about how long it would take.
+// The times are fits to measured ones (within a fifth from 9 to 1000 tokens); they only have to
+// rank the choices.
+struct PairPlan {
+  int W, tiles_m, tiles_n;
+  double ns;
+};
+struct SplitPlan {
+  int T, tiles_m, tiles_n, splits, slabs_per, per_sm;
+  double ns;
+};
+
+// Tile width: rounds of resident pairs, each of `slabs` slabs at the MMA's time for that width (four
+// of 107 cycles at 128 channels and 128 at 256), and a fixed cost for filling and draining.
+PairPlan plan_pair(const MatmulArgs& g, int sms) {
+  const int pairs = std::max(1, sms / 2), slabs = (g.K + 127) / 128;
+  PairPlan best = {0, (g.M + 255) / 256, 0, 0.0};
+  for (int w = 256; w >= 64; w -= 64) {
+    const int tiles_n = (g.N + w - 1) / w;
+    const int64_t rounds = ((int64_t)best.tiles_m * tiles_n + pairs - 1) / pairs;
+    const double ns = 4500.0 + rounds * (800.0 + slabs * (344 + w * 0.656) * 0.63);
+    if (best.W == 0 || ns < best.ns) best = {w, best.tiles_m, tiles_n, ns};
+  }
+  return best;
+}
+
+// CTAs of a tile (the cluster): as few rounds of resident CTAs, and slabs per round, as there can be.
+// Clusters of more than two leave some SMs of a graphics cluster unused (an eighth covers sizes up
+// to 6; 7 and 8 fit worse).
+SplitPlan plan_split(const MatmulArgs& g, int sms) {
+  const int slabs = (g.K + 127) / 128, tiles_m = (g.M + 255) / 256, tiles_n = (g.N + 127) / 128;
+  const int T = ((g.M + tiles_m - 1) / tiles_m + 15) / 16 * 16;
+  const int per_sm = T <= 128 ? 2 : 1;  // by shared memory, with at least three stages
+  SplitPlan best = {T, tiles_m, tiles_n, 0, 0, per_sm, 0.0};
+  for (int c = 1; c <= std::min(6, slabs); ++c) {
+    const int64_t room = std::max(1, (c <= 2 ? sms : sms * 7 / 8) * per_sm / c);
+    const int64_t rounds = ((int64_t)tiles_m * tiles_n + room - 1) / room;
+    const int each = (slabs + c - 1) / c;
+    const double ns = 5500.0 + 12.0 * T + rounds * each * (550.0 + 0.8 * T);
+    if (best.splits == 0 || ns < best.ns) best = {T, tiles_m, tiles_n, (slabs + each - 1) / each, each, per_sm, ns};
+  }
+  return best;
+}
+
 template <typename O, int kEpi>
-qbsa_status matmul_i8_pair(const MatmulArgs& g, int sms, cudaStream_t s) {
+qbsa_status matmul_i8_pair(const MatmulArgs& g, const PairPlan& plan, int sms, cudaStream_t s) {
   using C = qbsa::MatmulPairCfg<kEpi>;
   qbsa::MatmulPairParams prm;
   memset(&prm, 0, sizeof(prm));
-  const int pairs = std::max(1, sms / 2);
-  prm.tiles_m = (g.M + 255) / 256;
+  prm.W = plan.W;
+  prm.tiles_m = plan.tiles_m;
+  prm.tiles_n = plan.tiles_n;
   prm.slabs = (g.K + 127) / 128;
-  // Tile width: rounds of resident pairs, each of `slabs` slabs at the MMA's time for that width (four
-  // of 107 cycles at 128 channels and 128 at 256), and a fixed cost for filling and draining.
-  int64_t best = INT64_MAX;
-  for (int w = 256; w >= 64; w -= 64) {
-    const int64_t tiles = (int64_t)prm.tiles_m * ((g.N + w - 1) / w);
-    const int64_t cost = (tiles + pairs - 1) / pairs * (prm.slabs * (344 + w * 21 / 32) + 1500);
-    if (cost < best) {
-      best = cost;
-      prm.W = w;
-    }
-  }
-  prm.tiles_n = (g.N + prm.W - 1) / prm.W;
   prm.stage_bytes = C::kABytes + prm.W / 2 * 128;
   prm.stages = std::min(C::kMaxStages, C::kRingBytes / prm.stage_bytes);
   prm.a_scale = g.a_scale;
@@ -879,50 +912,31 @@ qbsa_status matmul_i8_pair(const MatmulArgs& g, int sms, cudaStream_t s) {
   prm.o_stride = g.o_stride;
   prm.M = g.M;
   prm.N = g.N;
+  prm.out_vec = aligned16(g.out) && (g.M == 1 || g.o_stride * sizeof(O) % 16 == 0);
   qbsa_status st;
   if ((st = make_map_2d(&prm.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.K, g.M, g.a_stride, 128, 128)) != QBSA_OK)
     return st;
   if ((st = make_map_2d(&prm.tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b, g.K, g.N, g.b_stride, 128, prm.W / 2)) != QBSA_OK)
     return st;
-  const uint64_t pitch = g.o_stride * sizeof(O);
-  prm.out_vec = aligned16(g.out) && pitch % 16 == 0;
   static std::atomic<uint64_t> done{0};
   if ((st = set_smem_once(qbsa::matmul_i8_pair_kernel<O, kEpi>, C::kSmemBytes, done)) != QBSA_OK) return st;
   const int64_t tiles = (int64_t)prm.tiles_m * prm.tiles_n;
-  const unsigned grid = 2u * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
+  const unsigned grid = 2u * static_cast<unsigned>(std::min<int64_t>(tiles, std::max(1, sms / 2)));
   qbsa::matmul_i8_pair_kernel<O, kEpi><<<grid, C::kThreads, C::kSmemBytes, s>>>(prm);
   return check_launch("matmul_i8_pair_kernel launch");
 }
 
 template <typename O>
-qbsa_status matmul_i8_split(const MatmulArgs& g, int sms, cudaStream_t s) {
+qbsa_status matmul_i8_split(const MatmulArgs& g, const SplitPlan& plan, cudaStream_t s) {
   using C = qbsa::MatmulSplitCfg;
   qbsa::MatmulSplitParams prm;
   memset(&prm, 0, sizeof(prm));
-  const int tiles_m = (g.M + 255) / 256;
-  prm.T = ((g.M + tiles_m - 1) / tiles_m + 15) / 16 * 16;
-  const int tiles_n = (g.N + 127) / 128;
+  prm.T = plan.T;
   prm.slabs = (g.K + 127) / 128;
+  prm.slabs_per = plan.slabs_per;
   prm.stage_bytes = C::kWBytes + prm.T * 128;
-  const int per_sm = prm.T <= 64 ? 2 : 1;
-  const int room = 232448 / per_sm - (per_sm > 1 ? 1024 : 0) - 1024 - C::kTailBytes;  // 1 KB a CTA is the system's
+  const int room = 232448 / plan.per_sm - (plan.per_sm > 1 ? 1024 : 0) - 1024 - C::kTailBytes;  // 1 KB a CTA is the system's
   prm.stages = std::min(C::kMaxStages, room / prm.stage_bytes);
-  // CTAs of a tile (the cluster): as few rounds of resident CTAs, and slabs per round, as there can
-  // be; a round's fixed cost is about six slabs.  Clusters of more than two leave some SMs of a
-  // graphics cluster unused (an eighth covers sizes up to 6; 7 and 8 fit worse).
-  const int64_t tiles = (int64_t)tiles_m * tiles_n;
-  int splits = 1;
-  int64_t best = INT64_MAX;
-  for (int c = 1; c <= std::min(6, prm.slabs); ++c) {
-    const int64_t room = std::max(1, (c <= 2 ? sms : sms * 7 / 8) * per_sm / c);
-    const int64_t cost = (tiles + room - 1) / room * ((prm.slabs + c - 1) / c + 6);
-    if (cost < best) {
-      best = cost;
-      splits = c;
-    }
-  }
-  prm.slabs_per = (prm.slabs + splits - 1) / splits;
-  splits = (prm.slabs + prm.slabs_per - 1) / prm.slabs_per;
   prm.tmem_cols = 32;
   while (prm.tmem_cols < prm.T) prm.tmem_cols *= 2;
   prm.a_scale = g.a_scale;
@@ -933,7 +947,6 @@ qbsa_status matmul_i8_split(const MatmulArgs& g, int sms, cudaStream_t s) {
   prm.M = g.M;
   prm.N = g.N;
   prm.vec = aligned_to(g.out, 4 * sizeof(O)) && (g.M == 1 || g.o_stride % 4 == 0);
-  if (tiles_n > 65535 || tiles_m > 65535) return fail(QBSA_ERR_UNSUPPORTED, "too many output tiles");
   qbsa_status st;
   if ((st = make_map_2d(&prm.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.K, g.M, g.a_stride, 128, prm.T)) != QBSA_OK)
     return st;
@@ -943,12 +956,12 @@ qbsa_status matmul_i8_split(const MatmulArgs& g, int sms, cudaStream_t s) {
   if ((st = set_smem_once(qbsa::matmul_i8_split_kernel<O>, 232448, done)) != QBSA_OK) return st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(splits);
+  attr.val.clusterDim.x = static_cast<unsigned>(plan.splits);
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(splits, tiles_n, tiles_m);
+  cfg.gridDim = dim3(plan.splits, plan.tiles_n, plan.tiles_m);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = prm.stages * prm.stage_bytes + C::kTailBytes + 1024;
   cfg.stream = s;
@@ -958,6 +971,8 @@ qbsa_status matmul_i8_split(const MatmulArgs& g, int sms, cudaStream_t s) {
   return e == cudaSuccess ? QBSA_OK : cuda_fail(e, "matmul_i8_split_kernel launch");
 }
 
+// 512 threads per 16 channels where there are at most as many CTAs as SMs (4.4 us against 5.6 at
+// 1 x 1024 x 5120), else 256 (7.8 against 11.1 at 1 x 5120 x 5120).
 template <typename O>
 qbsa_status matmul_i8_rows(const MatmulArgs& g, int sms, cudaStream_t s) {
   const qbsa::MatmulRowsParams prm = {g.a,  g.b,        g.a_scale,  g.b_scale,  g.bias, g.out,
@@ -968,14 +983,21 @@ qbsa_status matmul_i8_rows(const MatmulArgs& g, int sms, cudaStream_t s) {
   return check_launch("matmul_i8_rows_kernel launch");
 }
 
+// Up to 8 tokens: warp-level MMAs.  Else the tensor-core kernel that the plans find faster.  The pair
+// kernel takes eight epilogue warps instead of four (and a stage less) where a tile's multiplication
+// is too short to hide four, and where rows of out go out value by value (61 us against 78 at
+// 4000 x 5003 x 2000; equal from K = 10240 on).
 template <typename O>
 qbsa_status matmul_i8_launch(const MatmulArgs& g, cudaStream_t s) {
   int sms = 0;
   const qbsa_status st = sm_count(&sms);
   if (st != QBSA_OK) return st;
   if (g.M <= 8) return matmul_i8_rows<O>(g, sms, s);
-  if (g.M <= 256) return matmul_i8_split<O>(g, sms, s);
-  return g.K <= 1024 ? matmul_i8_pair<O, 8>(g, sms, s) : matmul_i8_pair<O, 4>(g, sms, s);
+  const PairPlan pair = plan_pair(g, sms);
+  const SplitPlan split = plan_split(g, sms);
+  if (split.ns < pair.ns && split.tiles_n <= 65535 && split.tiles_m <= 65535) return matmul_i8_split<O>(g, split, s);
+  const bool rows16 = aligned16(g.out) && g.o_stride * sizeof(O) % 16 == 0;
+  return g.K <= 1024 || !rows16 ? matmul_i8_pair<O, 8>(g, pair, sms, s) : matmul_i8_pair<O, 4>(g, pair, sms, s);
 }
 
 // The checks and launch that qbsa_rms_norm_quant and qbsa_quantize_token share.
