@@ -327,7 +327,7 @@ def _call_on(dev, fn, *args):
     """A library call on CUDA device `dev`'s current stream, with that device current."""
     import torch
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -378,14 +378,18 @@ def rms_norm_quant(x, weight, eps: float = 1e-6, *, residual=None, residual_out=
     _vector("weight", weight, width, dev, weight.dtype)
     r_ptr, rs, h_ptr, hs = None, 0, None, 0
     if residual is not None:
+        given = [("residual", residual)]
         if residual_out is None:
             import torch
-            residual_out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
-        for name, t in (("residual", residual), ("residual_out", residual_out)):
+            residual_out, hs = torch.empty_like(x, memory_format=torch.contiguous_format), width
+        else:
+            given.append(("residual_out", residual_out))
+            hs = _rows("residual_out", residual_out)[1]
+        for name, t in given:
             if t.dtype != x.dtype or t.shape != x.shape or t.get_device() != dev:
                 raise ValueError(f"{name} must have x's shape, type and device")
         r_ptr, rs = residual.data_ptr(), _rows("residual", residual)[1]
-        h_ptr, hs = residual_out.data_ptr(), _rows("residual_out", residual_out)[1]
+        h_ptr = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out is given with a residual only")
     _call_on(dev, lib().qbsa_rms_norm_quant, x.data_ptr(), xs, r_ptr, rs, weight.data_ptr(), code, wcode, rows, width,

@@ -263,29 +263,39 @@ __device__ __forceinline__ void store_codes(int8_t* p, int n, const uint32_t (&c
     if (i < n) p[i] = static_cast<int8_t>(c[i]);
 }
 
-// Sum and maximum over the threads of a row.  `a` is a magnitude's bits: unsigned order is the
-// order of the magnitudes, with infinity and then NaN above every number.
-// Several calls of a kernel take the two buffers in turn, with one barrier each.
-__device__ __forceinline__ void row_reduce(int group, float& sum, uint32_t& a, int buffer = 0) {
-  for (int o = min(group, 32) >> 1; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+// Sum (with a norm) and maximum over the threads of a row.  `a` is a magnitude's bits: unsigned order
+// is the order of the magnitudes, with infinity and then NaN above every number.
+template <bool kNorm>
+__device__ __forceinline__ void row_reduce_group(int group, float& sum, uint32_t& a) {
+  if (group == 32) {
+    a = __reduce_max_sync(0xffffffffu, a);
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    return;
+  }
+  for (int o = group >> 1; o > 0; o >>= 1) {
+    if constexpr (kNorm) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
   }
-  if (group <= 32) return;
-  __shared__ float red_sum_of[2][32];
-  __shared__ uint32_t red_max_of[2][32];
-  float* red_sum = red_sum_of[buffer];
-  uint32_t* red_max = red_max_of[buffer];
+}
+
+// The same over a CTA.  Several calls of a kernel take the two buffers in turn, with one barrier each.
+template <bool kNorm>
+__device__ __forceinline__ void row_reduce_cta(float& sum, uint32_t& a, int buffer) {
+  __shared__ float red_sum[2][32];
+  __shared__ uint32_t red_max[2][32];
+  row_reduce_group<kNorm>(32, sum, a);
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   if (lane == 0) {
-    red_sum[threadIdx.x >> 5] = sum;
-    red_max[threadIdx.x >> 5] = a;
+    if constexpr (kNorm) red_sum[buffer][threadIdx.x >> 5] = sum;
+    red_max[buffer][threadIdx.x >> 5] = a;
   }
   __syncthreads();
-  sum = lane < warps ? red_sum[lane] : 0.f;
-  a = lane < warps ? red_max[lane] : 0u;
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  a = __reduce_max_sync(0xffffffffu, a);
+  if constexpr (kNorm) sum = lane < warps ? red_sum[buffer][lane] : 0.f;
+  a = lane < warps ? red_max[buffer][lane] : 0u;
+  row_reduce_group<kNorm>(32, sum, a);
 }
 
 // Whether a row's values are numbers; their step s and its reciprocal for int8_code_byte.
@@ -442,58 +452,50 @@ __device__ __forceinline__ void write_codes(const NormQuantParams& p, int64_t ro
 constexpr float kOverflowUnit = 5.421010862427522e-20f;  // 2^-64
 __device__ __forceinline__ bool squares_overflow(bool numbers, float sum) { return numbers && !(sum <= 3.4e38f); }
 
-// Narrow rows: p.group <= 32 threads per row, kRows rows per group with their loads in flight
-// together (one row per thread in flight is too little for HBM's latency: 27 % of its bandwidth
-// at 65536 x 128 bf16).
-template <typename T, bool kNorm, bool kRes, int E, int kChunks, int kRows>
+// Narrow rows: p.group <= 32 threads per row, several rows per CTA, no barrier.  (A second row per
+// group with its loads in flight together cost more registers than it hid latency: 10.5 us against
+// 9.6 at 65536 x 128 bf16; one piece per thread in place of two: 11.8.)
+template <typename T, bool kNorm, bool kRes, int E, int kChunks>
 __global__ void __launch_bounds__(256) norm_quant_rows_kernel(const __grid_constant__ NormQuantParams p) {
   const int member = threadIdx.x & (p.group - 1);
-  const int64_t first = ((int64_t)blockIdx.x * (blockDim.x / p.group) + threadIdx.x / p.group) * kRows;
-  Piece<T, E> x[kRows][kChunks], q[kRows][kRes ? kChunks : 1];
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / p.group) + threadIdx.x / p.group;
+  const bool live = row < p.rows;
+  Piece<T, E> x[kChunks], q[kRes ? kChunks : 1];
 #pragma unroll
-  for (int j = 0; j < kRows; ++j)
+  for (int c = 0; c < kChunks; ++c) {
+    const int at = (c * p.group + member) * E, n = live ? p.width - at : 0;
+    x[c] = load_piece<T, E>(static_cast<const T*>(p.x) + row * p.x_stride + at, n);
+    if constexpr (kRes) q[c] = load_piece<T, E>(static_cast<const T*>(p.residual) + row * p.r_stride + at, n);
+  }
+  float g[kChunks][E];
+  float2 sum2 = make_float2(0.f, 0.f);
+  float a_own = 0.f;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int64_t row = first + j;
-      const int at = (c * p.group + member) * E, n = row < p.rows ? p.width - at : 0;
-      x[j][c] = load_piece<T, E>(static_cast<const T*>(p.x) + row * p.x_stride + at, n);
-      if constexpr (kRes) q[j][c] = load_piece<T, E>(static_cast<const T*>(p.residual) + row * p.r_stride + at, n);
-    }
-#pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    const int64_t row = first + j;
-    const bool live = row < p.rows;
-    float g[kChunks][E];
-    float2 sum2 = make_float2(0.f, 0.f);
-    float a_own = 0.f;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int at = (c * p.group + member) * E;
-      if (live && at < p.width)
-        take_values<T, kNorm, kRes, E>(p, row, at, p.width - at, x[j][c], q[j][kRes ? c : 0], g[c], sum2, a_own);
-    }
-    float sum = sum2.x + sum2.y;
-    uint32_t a = __float_as_uint(a_own);
-    row_reduce(p.group, sum, a);
-    float s, r, unit = 1.f;
-    const bool numbers = row_step(a, s, r);
-    if constexpr (kNorm) {
-      const bool again = squares_overflow(numbers, sum);  // the same in a row's threads
-      if (__any_sync(0xffffffffu, again)) {
-        __syncwarp();  // h of the row's other threads is written
-        float small = again && live ? sum_scaled<T, kRes>(p, row, member, p.group) : 0.f;
-        row_reduce(p.group, small, a);
-        if (again) {
-          sum = small;
-          unit = kOverflowUnit;
-        }
+  for (int c = 0; c < kChunks; ++c) {
+    const int at = (c * p.group + member) * E;
+    if (live && at < p.width)
+      take_values<T, kNorm, kRes, E>(p, row, at, p.width - at, x[c], q[kRes ? c : 0], g[c], sum2, a_own);
+  }
+  float sum = sum2.x + sum2.y;
+  uint32_t a = __float_as_uint(a_own);
+  row_reduce_group<kNorm>(p.group, sum, a);
+  float s, r, unit = 1.f;
+  const bool numbers = row_step(a, s, r);
+  if constexpr (kNorm) {
+    const bool again = squares_overflow(numbers, sum);  // the same in a row's threads
+    if (__any_sync(0xffffffffu, again)) {
+      __syncwarp();  // h of the row's other threads is written
+      float small = again && live ? sum_scaled<T, kRes>(p, row, member, p.group) : 0.f;
+      row_reduce_group<kNorm>(p.group, small, a);
+      if (again) {
+        sum = small;
+        unit = kOverflowUnit;
       }
     }
-    if (live) {
-      if (member == 0) p.scales[row] = row_scale<kNorm>(a, numbers, s, sum, unit, p.width, p.eps);
-      write_codes<T, kNorm, E, kChunks>(p, row, member, p.group, g, numbers, s, r);
-    }
   }
+  if (!live) return;
+  if (member == 0) p.scales[row] = row_scale<kNorm>(a, numbers, s, sum, unit, p.width, p.eps);
+  write_codes<T, kNorm, E, kChunks>(p, row, member, p.group, g, numbers, s, r);
 }
 
 // A CTA per row, the row in registers: kChunks pieces of E values per thread (E = 16 bytes of T,
@@ -521,17 +523,25 @@ __global__ void __launch_bounds__(kChunks * E > 16 ? 640 : 1024)
   }
   float sum = sum2.x + sum2.y;
   uint32_t a = __float_as_uint(a_own);
-  row_reduce(kNormWideThreads, sum, a);
+  row_reduce_cta<kNorm>(sum, a, 0);
   float s, r, unit = 1.f;
   const bool numbers = row_step(a, s, r);
   if (kNorm && squares_overflow(numbers, sum)) {  // the same in every thread
     __syncthreads();                               // h of the other threads is written
     sum = sum_scaled<T, kRes>(p, row, member, step);
-    row_reduce(kNormWideThreads, sum, a, 1);
+    row_reduce_cta<kNorm>(sum, a, 1);
     unit = kOverflowUnit;
   }
   if (member == 0) p.scales[row] = row_scale<kNorm>(a, numbers, s, sum, unit, p.width, p.eps);
   write_codes<T, kNorm, E, kChunks>(p, row, member, step, g, numbers, s, r);
+}
+
+// Two pieces of 16-bit rows with a residual need 64 registers a thread (82 us against 86 with 48 and
+// spills at 16384 x 4096), the others with two pieces run best at 48 and a third more threads (47 us
+// against 49 for the quantiser alone at 16384 x 5120).
+template <typename T, bool kRes, int kChunks>
+__host__ __device__ constexpr bool norm_stream_roomy() {
+  return kChunks == 2 && kRes && sizeof(T) == 2;
 }
 
 // Many rows: the grid stays resident and each CTA takes every gridDim.x-th row, its next rows on
@@ -543,7 +553,7 @@ __global__ void __launch_bounds__(kChunks * E > 16 ? 640 : 1024)
 // rows, whose units may reach beyond it, are read in place.  Rows do not overlap then.  (Value by value, coalesced,
 // such rows ran at 20 % of HBM's bandwidth, bound by their instructions.)
 template <typename T, bool kNorm, bool kRes, int kChunks, bool kAligned>
-__global__ void __launch_bounds__(kChunks == 4 ? 640 : 512)
+__global__ void __launch_bounds__(norm_stream_roomy<T, kRes, kChunks>() ? 512 : 640, kChunks == 2 ? 2 : 1)
     norm_quant_stream_kernel(const __grid_constant__ NormQuantParams p) {
   constexpr int E = 16 / sizeof(T);
   extern __shared__ __align__(128) uint8_t ring[];
@@ -631,7 +641,7 @@ __global__ void __launch_bounds__(kChunks == 4 ? 640 : 512)
     }
     float sum = sum2.x + sum2.y;
     uint32_t a = __float_as_uint(a_own);
-    row_reduce(kNormWideThreads, sum, a, it & 1);
+    row_reduce_cta<kNorm>(sum, a, it & 1);
     if (tid == 0) {
       const int64_t next = row + (int64_t)p.stages * gridDim.x;
       if (next < p.rows && !*static_cast<volatile int*>(&abort_flag)) {
@@ -671,7 +681,7 @@ __global__ void __launch_bounds__(kChunks == 4 ? 640 : 512)
     if (kNorm && squares_overflow(numbers, sum)) {  // the same in every thread
       __syncthreads();
       sum = sum_scaled<T, kRes>(p, row, tid, step);
-      row_reduce(kNormWideThreads, sum, a, it & 1);
+      row_reduce_cta<kNorm>(sum, a, it & 1);
       unit = kOverflowUnit;
       __syncthreads();
     }
@@ -700,13 +710,13 @@ __global__ void __launch_bounds__(kNormWideThreads) norm_quant_wide_kernel(const
   }
   float sum = sum2.x + sum2.y;
   uint32_t a = __float_as_uint(a_own);
-  row_reduce(kNormWideThreads, sum, a);
+  row_reduce_cta<kNorm>(sum, a, 0);
   float s, r, unit = 1.f;
   const bool numbers = row_step(a, s, r);
   if (kNorm && squares_overflow(numbers, sum)) {
     __syncthreads();
     sum = sum_scaled<T, kRes>(p, row, threadIdx.x, kNormWideThreads);
-    row_reduce(kNormWideThreads, sum, a, 1);
+    row_reduce_cta<kNorm>(sum, a, 1);
     unit = kOverflowUnit;
   }
   if (threadIdx.x == 0) p.scales[row] = row_scale<kNorm>(a, numbers, s, sum, unit, p.width, p.eps);
