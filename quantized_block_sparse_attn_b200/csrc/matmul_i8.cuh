@@ -10,12 +10,11 @@
 #include <cuda.h>
 
 #include "norm_quant.cuh"
-#include "ptx_sm100.cuh"
+#include "ptx_cluster.cuh"
 
 namespace qbsa {
 
 constexpr int kMatmulMaxK = 131071;  // 2^14 K < 2^31
-
 
 // f32 from the exact sum, by the rule above.
 __device__ __forceinline__ float scale_acc(uint32_t acc, float sa, float sb, float bias) {
@@ -255,7 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MatmulPairCfg<kEpi>:
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     constexpr int kCols = 128 / sizeof(O);  // columns of a staged piece
-    constexpr int kTurns = kEpi / 4;            // the warps of a quarter take a tile's pieces in turn
+    constexpr int kTurns = kEpi / 4;        // the warps of a quarter take a tile's pieces in turn
     const int quarter = warp & 3, own = warp - 4, first = own / 4 * kCols;
     const uint32_t stage = base + C::kOutOff + own * C::kOutBytes;
     float* col = reinterpret_cast<float*>(smem + C::kColOff + own * C::kColBytes);

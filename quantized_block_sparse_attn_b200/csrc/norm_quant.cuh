@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "ptx_cluster.cuh"
 #include "quantize.cuh"
 
 namespace qbsa {
@@ -536,14 +537,6 @@ __global__ void __launch_bounds__(kChunks * E > 16 ? 640 : 1024)
   write_codes<T, kNorm, E, kChunks>(p, row, member, step, g, numbers, s, r);
 }
 
-// Two pieces of 16-bit rows with a residual need 64 registers a thread (82 us against 86 with 48 and
-// spills at 16384 x 4096), the others with two pieces run best at 48 and a third more threads (47 us
-// against 49 for the quantiser alone at 16384 x 5120).
-template <typename T, bool kRes, int kChunks>
-__host__ __device__ constexpr bool norm_stream_roomy() {
-  return kChunks == 2 && kRes && sizeof(T) == 2;
-}
-
 // Many rows: the grid stays resident and each CTA takes every gridDim.x-th row, its next rows on
 // their way into a ring in shared memory by bulk copies.  The reduction's barrier also says that
 // every thread has read the row, so its stage is refilled right behind it.
@@ -552,8 +545,12 @@ __host__ __device__ constexpr bool norm_stream_roomy() {
 // units each, and h goes out by its own units through shared memory; the tensor's first and last
 // rows, whose units may reach beyond it, are read in place.  Rows do not overlap then.  (Value by value, coalesced,
 // such rows ran at 20 % of HBM's bandwidth, bound by their instructions.)
+// Four pieces per thread: what a row costs its warps beside its values (the reduction, the step) is
+// shared by more values (42 us against 49 with two pieces for the quantiser alone at 16384 x 5120
+// bf16, 382 against 395 at 65536 x 5120 with a residual; eight: 48 and 432).  Two for unaligned rows
+// with a residual (134 against 143 at 16384 x 4097).
 template <typename T, bool kNorm, bool kRes, int kChunks, bool kAligned>
-__global__ void __launch_bounds__(norm_stream_roomy<T, kRes, kChunks>() ? 512 : 640, kChunks == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kChunks == 4 ? 640 : 512, kChunks == 4 ? 1 : 2)
     norm_quant_stream_kernel(const __grid_constant__ NormQuantParams p) {
   constexpr int E = 16 / sizeof(T);
   extern __shared__ __align__(128) uint8_t ring[];
@@ -620,7 +617,7 @@ __global__ void __launch_bounds__(norm_stream_roomy<T, kRes, kChunks>() ? 512 : 
   int it = 0, s = 0, phase = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, ++it) {
     // a wait that runs out is reported; the CTA goes on, so that its barriers stay in step
-    mbar_wait(smem_u32(&full[s]), phase, &abort_flag);
+    mbar_wait_hot(smem_u32(&full[s]), phase, &abort_flag);
     float g[kChunks][E];
     float2 sum2 = make_float2(0.f, 0.f);
     float a_own = 0.f;

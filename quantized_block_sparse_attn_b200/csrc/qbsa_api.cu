@@ -780,9 +780,7 @@ qbsa_status launch_norm_stream(qbsa::NormQuantParams& prm, int threads, cudaStre
   if (st != QBSA_OK) return st;
   const int64_t slot = qbsa::stream_slot_bytes<T>(prm.width, kAligned);
   const int64_t stage = slot * (kRes ? 2 : 1), staged = kRes && !kAligned ? 2 * slot : 0;
-  // by registers: 64, 48 or 96 a thread
-  const int resident = qbsa::norm_stream_roomy<T, kRes, kChunks>() ? 1024 : kChunks == 2 ? 1365 : 682;
-  int per_sm = std::max(1, std::min(32, resident / threads));
+  int per_sm = std::max(1, std::min(32, (kChunks == 4 ? 682 : 1024) / threads));  // 96 or 64 registers
   while (per_sm > 1 && (2 * stage + staged) * per_sm > kNormRingBytes) --per_sm;
   prm.stages = static_cast<int>(std::min<int64_t>(qbsa::kNormMaxStages, (kNormRingBytes / per_sm - staged) / stage));
   if (prm.stages < 2 || prm.rows <= (int64_t)sms * per_sm) return QBSA_OK;
@@ -816,13 +814,11 @@ qbsa_status launch_norm_quant(qbsa::NormQuantParams& prm, bool vec, cudaStream_t
   if (!vec && prm.width <= 256) return launch_norm_rows<T, kNorm, kRes, 1, 8>(prm, prm.width, s);
   bool taken = false;
   if (pieces <= 2560) {
-    const bool aligned = vec && prm.width % E == 0;
-    const int each = pieces <= 1024 ? 2 : 4, n = threads(pieces, each);
-    const qbsa_status st =
-        each == 2 ? (aligned ? launch_norm_stream<T, kNorm, kRes, 2, true>(prm, n, s, &taken)
-                             : launch_norm_stream<T, kNorm, kRes, 2, false>(prm, n, s, &taken))
-                  : (aligned ? launch_norm_stream<T, kNorm, kRes, 4, true>(prm, n, s, &taken)
-                             : launch_norm_stream<T, kNorm, kRes, 4, false>(prm, n, s, &taken));
+    const int each = pieces <= 1024 ? 2 : 4, n = threads(pieces, each), n4 = threads(pieces, 4);
+    qbsa_status st = QBSA_OK;
+    if (vec && prm.width % E == 0) st = launch_norm_stream<T, kNorm, kRes, 4, true>(prm, n4, s, &taken);
+    else if (!kRes || each == 4) st = launch_norm_stream<T, kNorm, kRes, 4, false>(prm, n4, s, &taken);
+    else if constexpr (kRes) st = launch_norm_stream<T, kNorm, kRes, 2, false>(prm, n, s, &taken);
     if (taken || st != QBSA_OK) return st;
     if (vec && each == 2) return launch_norm_cta<T, kNorm, kRes, E, 2>(prm, n, s);
     if (vec) return launch_norm_cta<T, kNorm, kRes, E, 4>(prm, n, s);

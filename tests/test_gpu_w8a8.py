@@ -12,6 +12,11 @@ Tolerances.  u = 2^-24 is half a step of float32.
   are 3 u of |product| + |bias|, then half a step of the output's type.
 """
 
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -433,6 +438,68 @@ def test_layer_captured_and_replayed():
         graph.replay()
         for g, e in zip(got, w):
             assert torch.equal(g, e)
+    qb.check()
+
+
+def test_first_use_inside_a_capture():
+    """A process whose first calls of these kernels are captured: no allocation, no set-up that a capture
+    forbids."""
+    script = """
+import sys, torch
+sys.path.insert(0, %r)
+import quantized_block_sparse_attn_b200 as qb
+torch.manual_seed(0)
+x = torch.randn((600, 1024), device="cuda").bfloat16()
+w = torch.ones(1024, device="cuda", dtype=torch.bfloat16)
+b = torch.randint(-127, 128, (384, 1024), device="cuda").to(torch.int8)
+sb = torch.rand(384, device="cuda")
+torch.cuda.synchronize()
+def run():
+    c, s, h = qb.rms_norm_quant(x, w, residual=x)
+    return [c, s, h] + [qb.matmul_i8(c[:m], b, s[:m], sb) for m in (1, 40, 600)]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+for a, e in zip(got, run()):
+    assert torch.equal(a, e)
+qb.check()
+print("captured")
+""" % os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", script], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_threads_at_once():
+    """Calls from two host threads, each on its own stream."""
+    a, b = _codes(1, 300, 1024), _codes(2, 700, 1024)
+    sa, sb = torch.rand(300, device="cuda") + 0.5, torch.rand(700, device="cuda")
+    x, w = _randn(3, (300, 1024), BF16), _randn(4, (1024,), BF16)
+    want = (qb.matmul_i8(a, b, sa, sb), *qb.rms_norm_quant(x, w, residual=x))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got = (qb.matmul_i8(a, b, sa, sb), *qb.rms_norm_quant(x, w, residual=x))
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(g, e) for g, e in zip(got, want)):
+                    bad.append(1)
+                try:
+                    qb.rms_norm_quant(x, w, -1.0)
+                    bad.append(2)
+                except qb.QbsaError as e:
+                    if "eps" not in str(e):
+                        bad.append(3)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
     qb.check()
 
 
