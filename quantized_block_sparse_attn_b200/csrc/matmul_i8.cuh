@@ -171,7 +171,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MatmulPairCfg<kEpi>:
     // ---------------------------------------------------------------- producer
     if (lane == 0) {
       const uint32_t full0 = cluster_map(bar(C::kBarFull), 0);  // the even CTA's barriers
-      const uint64_t pol_a = l2_policy_evict_first(), pol_b = l2_policy_evict_last();
+      // B is read again by every group of tile rows; with one group it is A that is read again
+      const bool one_group = p.tiles_m <= C::kGroupM;
+      const uint64_t pol_a = one_group ? l2_policy_evict_last() : l2_policy_evict_first();
+      const uint64_t pol_b = one_group ? l2_policy_evict_first() : l2_policy_evict_last();
       const uint32_t bytes = 2u * static_cast<uint32_t>(p.stage_bytes);
       const int slabs = p.slabs, stages = p.stages;
       int it = 0, s = 0;
