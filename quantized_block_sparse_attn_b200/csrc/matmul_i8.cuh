@@ -393,7 +393,8 @@ struct MatmulSplitCfg {
   static constexpr int kBarEmpty = kBarFull + kMaxStages;
   static constexpr int kBarAccFull = kBarEmpty + kMaxStages;
   static constexpr int kNumBars = kBarAccFull + 1;
-  static constexpr int kTailBytes = kNumBars * 8 + 16;  // barriers, TMEM address, abort flag
+  static constexpr int kScalesOff = kNumBars * 8 + 24;       // after barriers, TMEM address, abort flag
+  static constexpr int kTailBytes = kScalesOff + 256 * 4;  // a_scale of the tile's tokens
 };
 
 template <typename O>
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
   const int n0 = blockIdx.y * 128, m0 = blockIdx.z * p.T;
   const int k0 = rank * p.slabs_per, slabs = min(p.slabs_per, p.slabs - k0);
 
-  // this lane's channels and this warp's first token: fetched while the sums are made
+  // scales of this lane's channels and of the tile's tokens: fetched while the sums are made
   const int n = n0 + 4 * lane, tokens = min(p.T, p.M - m0);
   float sb[4], bi[4];
 #pragma unroll
@@ -422,7 +423,8 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
     sb[i] = n + i < p.N ? p.b_scale[n + i] : 0.f;
     bi[i] = n + i < p.N && p.bias ? p.bias[n + i] : 0.f;
   }
-  float sa = rank + splits * warp < tokens ? p.a_scale[m0 + rank + splits * warp] : 0.f;
+  float* a_scales = reinterpret_cast<float*>(smem + tail + C::kScalesOff);
+  for (int t = threadIdx.x; t < tokens; t += C::kThreads) a_scales[t] = p.a_scale[m0 + t];
   bool acc_ok = false;
 
   const uint64_t pol_w = l2_policy_evict_first(), pol_t = l2_policy_evict_last();
@@ -495,7 +497,8 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
   // ------------------------------------------------------------------ sums to their owners
   // Token t belongs to CTA t % splits, which gets [splits][per][128] sums.  Stores to the other
   // CTAs, so that no warp waits for a remote load (each CTA reading its share from the others took
-  // 21.6 us at 256 x 5120 x 5120, this 18.3).
+  // 21.6 us at 256 x 5120 x 5120, this 18.0), of 128 neighbouring bytes per warp (16 bytes a lane,
+  // four tokens of a channel: 18.1 there, and 10.4 against 9.6 at 16 x 6144 x 4096).
   const int per = (p.T + splits - 1) / splits;
   if (warp < 4 && acc_ok) {
     int owner = 0, idx = 0;
@@ -520,8 +523,8 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
   // ------------------------------------------------------------------ joined, scaled and stored
   // a warp takes a token, a lane four channels
   for (int idx = warp; rank + splits * idx < tokens; idx += C::kThreads / 32) {
-    const int m = m0 + rank + splits * idx;
-    if (idx != warp) sa = p.a_scale[m];
+    const int t = rank + splits * idx;
+    const float sa = a_scales[t];
     int4 v = make_int4(0, 0, 0, 0);
     for (int c = 0; c < splits; ++c) {
       const uint4 u = lds128(base + static_cast<uint32_t>((c * per + idx) * 512 + 16 * lane));
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(MatmulSplitCfg::kThreads)
     }
     const float f[4] = {scale_acc(v.x, sa, sb[0], bi[0]), scale_acc(v.y, sa, sb[1], bi[1]),
                         scale_acc(v.z, sa, sb[2], bi[2]), scale_acc(v.w, sa, sb[3], bi[3])};
-    O* dst = static_cast<O*>(p.out) + m * p.o_stride + n;
+    O* dst = static_cast<O*>(p.out) + (m0 + t) * p.o_stride + n;
     if (p.vec && n + 4 <= p.N) {
       if constexpr (sizeof(O) == 4) *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
       else *reinterpret_cast<uint2*>(dst) = make_uint2(pack_out2<O>(f[0], f[1]), pack_out2<O>(f[2], f[3]));

@@ -849,8 +849,7 @@ struct MatmulArgs {
 };
 
 // How a product would be cut for the two tensor-core kernels, and about how long it would take.
-// The times are fits to measured ones (within a fifth from 9 to 1000 tokens); they only have to
-// rank the choices.
+// The times are fits to measured ones (mostly within a fifth); they only have to rank the choices.
 struct PairPlan {
   int W, tiles_m, tiles_n;
   double ns;
@@ -886,7 +885,8 @@ SplitPlan plan_split(const MatmulArgs& g, int sms) {
     const int64_t room = std::max(1, (c <= 2 ? sms : sms * 7 / 8) * per_sm / c);
     const int64_t rounds = ((int64_t)tiles_m * tiles_n + room - 1) / room;
     const int each = (slabs + c - 1) / c;
-    const double ns = 5500.0 + 12.0 * T + rounds * each * (550.0 + 0.8 * T);
+    // a round's fill, slabs, and sums on their way out (the last grow with the tokens of a CTA)
+    const double ns = 2500.0 + rounds * (2500.0 + each * (550.0 + 0.8 * T) + 10.0 * T + 0.2 * T * T / c);
     if (best.splits == 0 || ns < best.ns) best = {T, tiles_m, tiles_n, (slabs + each - 1) / each, each, per_sm, ns};
   }
   return best;
