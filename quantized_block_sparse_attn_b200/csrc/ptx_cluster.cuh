@@ -90,6 +90,20 @@ __device__ __forceinline__ void st_cluster_b32(uint32_t cluster_addr, uint32_t v
 // loads
 // ---------------------------------------------------------------------------------
 
+// A 2- or 4-byte value of shared memory, as bits.
+template <int kBytes>
+__device__ __forceinline__ uint32_t lds_value(uint32_t addr) {
+  if constexpr (kBytes == 2) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+  } else {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+  }
+}
+
 // `bytes` contiguous bytes (a multiple of 16, both ends 16-byte aligned) into this CTA's shared
 // memory; completes on an mbarrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
