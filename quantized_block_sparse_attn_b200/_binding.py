@@ -350,7 +350,11 @@ def _token_arguments(x, codes, scales):
             codes, cs = torch.empty_like(x, dtype=torch.int8), width
         else:
             cs = -(-width // 16) * 16
-            codes = x.new_empty((*shape[:-1], cs), dtype=torch.int8)[..., :width]
+            strides, n = [1], cs
+            for d in reversed(shape[:-1]):
+                strides.append(n)
+                n *= d
+            codes = torch.empty_strided(shape, strides[::-1], dtype=torch.int8, device=x.device)
     else:
         if codes.dtype != torch.int8 or codes.shape != shape or codes.get_device() != dev:
             raise ValueError("codes must be an int8 tensor of x's shape on x's device")

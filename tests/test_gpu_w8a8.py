@@ -230,6 +230,75 @@ def test_leading_dimensions_and_one_row():
     _check_tokens(c, s, x[0, 0].expand(4, 40))
 
 
+def test_rows_that_overlap_in_memory():
+    """Windows over one buffer, by a row stride below the width (inputs only)."""
+    pool = _randn(1, (40000,), BF16)
+    w = _randn(2, (520,), BF16)
+    for stride, rows in ((8, 3000), (3, 3000), (1, 50), (0, 5)):
+        x = pool.as_strided((rows, 520), (stride, 1))
+        codes, scales, _ = qb.rms_norm_quant(x, w)
+        _check_tokens(codes, scales, x, w, 1e-6)
+        codes, scales, h = qb.rms_norm_quant(x, w, residual=x)
+        _check_tokens(codes, scales, h, w, 1e-6)
+    qb.check()
+
+
+@pytest.mark.parametrize("dtype,wdtype", [(BF16, FP32), (FP16, FP16), (FP32, FP32)])
+@pytest.mark.parametrize("rows", [3, 2000])
+def test_weight_off_a_16_byte_boundary(dtype, wdtype, rows):
+    pool = _randn(3, (1100,), wdtype)
+    for width in (520, 1031):
+        for off in (0, 1, 2):
+            x, w = _randn(4, (rows, width), dtype), pool[off:off + width]
+            codes, scales, h = qb.rms_norm_quant(x, w, residual=x)
+            _check_tokens(codes, scales, h, w, 1e-6)
+
+
+def test_no_tokens():
+    x, w = _randn(1, (4, 48), BF16), _randn(2, (48,), BF16)
+    c, s, h = qb.rms_norm_quant(x[:0], w, residual=x[:0])
+    assert c.shape == (0, 48) and s.shape == (0,) and h.shape == (0, 48)
+    b, sb = qb.quantize_token(x)
+    assert qb.matmul_i8(c, b, s, sb).shape == (0, 4)
+    assert qb.matmul_i8(b, c, sb, s).shape == (4, 0)
+    qb.check()
+
+
+def test_more_than_2_to_31_values():
+    """Row offsets past 32 bits: the last rows come out as they do alone."""
+    rows, width = 66000, 32776
+    x = torch.empty((rows, width), dtype=BF16, device="cuda")
+    x.normal_()
+    codes, scales = qb.quantize_token(x)
+    for part in (x[:3], x[-5:]):
+        at = 0 if part.data_ptr() == x.data_ptr() else rows - 5
+        c, s = qb.quantize_token(part.clone())
+        assert torch.equal(codes[at:at + len(part)], c) and torch.equal(scales[at:at + len(part)], s)
+    del x
+    a, b = codes[:, :64].contiguous(), codes[:width, :64].contiguous()
+    sa, sb = scales, scales[:width].contiguous()
+    out = qb.matmul_i8(a, b, sa, sb)
+    qb.check()
+    assert torch.equal(out[-5:], qb.matmul_i8(a[-5:], b, sa[-5:], sb))
+    assert torch.equal(out[-300:, -1000:], qb.matmul_i8(a[-300:], b[-1000:], sa[-300:], sb[-1000:]))
+    qb.check()
+
+
+def test_matmul_i8_leading_dimensions():
+    a, b = _codes(1, 12, 100), _codes(2, 70, 100)
+    sa, sb = torch.rand(12, device="cuda"), torch.rand(70, device="cuda")
+    want = qb.matmul_i8(a, b, sa, sb)
+    a3 = a.as_strided((3, 4, 100), (4 * a.stride(0), a.stride(0), 1))
+    assert torch.equal(qb.matmul_i8(a3, b, sa.view(3, 4), sb), want.view(3, 4, 70))
+    out = torch.zeros((3, 4, 80), dtype=BF16, device="cuda")
+    got = qb.matmul_i8(a3, b, sa.view(3, 4), sb, out=out[..., 5:75])
+    assert torch.equal(got, want.view(3, 4, 70)) and torch.all(out[..., :5] == 0) and torch.all(out[..., 75:] == 0)
+    assert torch.equal(qb.matmul_i8(a[5], b, sa[5:6], sb), want[5])
+    with pytest.raises(ValueError):
+        qb.matmul_i8(a3.transpose(0, 1), b, sa.view(3, 4), sb)
+    qb.check()
+
+
 def test_binding_refusals():
     x, w = _randn(1, (4, 64), BF16), _randn(2, (64,), BF16)
     for call in (
