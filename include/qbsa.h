@@ -338,11 +338,11 @@ qbsa_status qbsa_block_topk_keep(const float* q_mean, const float* k_mean, int B
 
 /*
  * qbsa_wait_selftest -- test hook for failure detection (no counterpart on the source
- * pages): launches one thread that waits, through the same bounded mbarrier wait every
- * kernel of this library uses, on a phase that nothing ever completes.  After the wait
- * limit (2 s) the thread records a timeout in the device error word and the kernel ends
- * normally, so the next qbsa_check(stream) returns QBSA_ERR_TIMEOUT and the context stays
- * usable.  No fault, trap or endless loop is involved.
+ * pages): launches two threads that wait, each through one of the two bounded mbarrier waits
+ * that the kernels of this library use, on phases that nothing ever completes.  After the wait
+ * limit (2 s) each records a timeout in the device error word and the kernel ends normally,
+ * so the next qbsa_check(stream) returns QBSA_ERR_TIMEOUT and the context stays usable.  No
+ * fault, trap or endless loop is involved.
  */
 qbsa_status qbsa_wait_selftest(void* stream);
 

@@ -1212,23 +1212,25 @@ qbsa_status qbsa_block_topk_keep(const float* q_mean, const float* k_mean, int B
 }
 
 namespace qbsa {
-// Failure-detection self-test: one thread waits, through the kernels' own bounded wait, on
-// an mbarrier phase that nothing completes; the wait gives up after its time limit, records
-// the timeout in the device error word and the kernel returns normally.
+// Failure-detection self-test: two threads wait, each through one of the kernels' bounded waits, on
+// mbarrier phases that nothing completes; the waits give up after their time limit, record the
+// timeout in the device error word and the kernel returns normally.
 __global__ void wait_selftest_kernel() {
-  __shared__ uint64_t barrier;
-  __shared__ int abort_flag;
-  if (threadIdx.x != 0) return;
-  abort_flag = 0;
-  const uint32_t bar = smem_u32(&barrier);
+  __shared__ uint64_t barrier[2];
+  __shared__ int abort_flag[2];
+  const int i = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) != 0) return;
+  abort_flag[i] = 0;
+  const uint32_t bar = smem_u32(&barrier[i]);
   mbar_init(bar, 1);
   fence_mbar_init();
-  mbar_wait(bar, 0, &abort_flag);  // no arrival ever comes
+  if (i == 0) mbar_wait(bar, 0, &abort_flag[i]);  // no arrival ever comes
+  else mbar_wait_hot(bar, 0, &abort_flag[i]);
 }
 }  // namespace qbsa
 
 qbsa_status qbsa_wait_selftest(void* stream) {
-  qbsa::wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>();
+  qbsa::wait_selftest_kernel<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>();
   return check_launch("wait_selftest_kernel launch");
 }
 
