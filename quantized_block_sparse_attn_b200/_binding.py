@@ -323,6 +323,11 @@ def _vector(name, t, n, dev, dtype):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on the input's device")
 
 
+def _alike(name, t, x, dev):
+    if t.dtype != x.dtype or t.shape != x.shape or t.get_device() != dev:
+        raise ValueError(f"{name} must have x's shape, type and device")
+
+
 def _call_on(dev, fn, *args):
     """A library call on CUDA device `dev`'s current stream, with that device current."""
     import torch
@@ -360,7 +365,7 @@ def _token_arguments(x, codes, scales):
             raise ValueError("codes must be an int8 tensor of x's shape on x's device")
         cs = _rows("codes", codes)[1]
     if scales is None:
-        scales = x.new_empty(rows if len(shape) == 2 else shape[:-1], dtype=torch.float32)
+        scales = torch.empty(rows if len(shape) == 2 else shape[:-1], dtype=torch.float32, device=x.device)
     else:
         _vector("scales", scales, rows, dev, torch.float32)
     return dev, code, codes, scales, rows, xs, cs
@@ -382,17 +387,14 @@ def rms_norm_quant(x, weight, eps: float = 1e-6, *, residual=None, residual_out=
     _vector("weight", weight, width, dev, weight.dtype)
     r_ptr, rs, h_ptr, hs = None, 0, None, 0
     if residual is not None:
-        given = [("residual", residual)]
+        _alike("residual", residual, x, dev)
+        r_ptr, rs = residual.data_ptr(), _rows("residual", residual)[1]
         if residual_out is None:
             import torch
             residual_out, hs = torch.empty_like(x, memory_format=torch.contiguous_format), width
         else:
-            given.append(("residual_out", residual_out))
+            _alike("residual_out", residual_out, x, dev)
             hs = _rows("residual_out", residual_out)[1]
-        for name, t in given:
-            if t.dtype != x.dtype or t.shape != x.shape or t.get_device() != dev:
-                raise ValueError(f"{name} must have x's shape, type and device")
-        r_ptr, rs = residual.data_ptr(), _rows("residual", residual)[1]
         h_ptr = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out is given with a residual only")
@@ -435,7 +437,11 @@ def matmul_i8(a, b, a_scale, b_scale, *, bias=None, out_dtype=None, out=None):
         code = _dtype_code(out_dtype)
         if code is None:
             raise ValueError("out_dtype must be bfloat16, float16 or float32")
-        out, so = a.new_empty((*a_shape[:-1], n), dtype=out_dtype), n
+        if len(a_shape) == 2:
+            out = torch.empty_strided((m, n), (n, 1), dtype=out_dtype, device=a.device)
+        else:
+            out = torch.empty((*a_shape[:-1], n), dtype=out_dtype, device=a.device)
+        so = n
     else:
         code = _dtype_code(out.dtype)
         if code is None or out_dtype not in (None, out.dtype):
