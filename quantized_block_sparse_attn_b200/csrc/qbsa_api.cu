@@ -992,8 +992,12 @@ qbsa_status matmul_i8_rows(const MatmulArgs& g, int sms, cudaStream_t s) {
 
 // Up to 8 tokens: warp-level MMAs.  Else the tensor-core kernel that the plans find faster.  The pair
 // kernel takes eight epilogue warps instead of four (and a stage less) where a tile's multiplication
-// is too short to hide four, and where rows of out go out value by value (61 us against 78 at
-// 4000 x 5003 x 2000; equal from K = 10240 on).
+// is too short to hide four.  Rows of out at any alignment are stored unit by unit, so there that lasts
+// to a K of 1280 per byte of O (eight against four, 4000 x 5003 x K: K = 2000 fp32 63.5 us against 70.0
+// and bf16 54.4 against 56.5, K = 2560 bf16 52.1 against 54.7; K = 3584 bf16 68.8 against 67.5, K = 5120
+// fp32 equal, K = 10240 bf16 169 against 164).  Aligned rows go out by 16-byte stores from their own
+// lanes, and only fp32 over two slabs has more to store than four can hide (16384 x 5120 x 256 80.5
+// against 83.9; 4096 x 5120 x 1024 34.7 against 34.3, and bf16 28.6 against 27.8).
 template <typename O>
 qbsa_status matmul_i8_launch(const MatmulArgs& g, cudaStream_t s) {
   int sms = 0;
@@ -1004,7 +1008,9 @@ qbsa_status matmul_i8_launch(const MatmulArgs& g, cudaStream_t s) {
   const SplitPlan split = plan_split(g, sms);
   if (split.ns < pair.ns && split.tiles_n <= 65535 && split.tiles_m <= 65535) return matmul_i8_split<O>(g, split, s);
   const bool rows16 = aligned16(g.out) && g.o_stride * sizeof(O) % 16 == 0;
-  return g.K <= 1024 || !rows16 ? matmul_i8_pair<O, 8>(g, pair, sms, s) : matmul_i8_pair<O, 4>(g, pair, sms, s);
+  const int size = sizeof(O);
+  const bool eight = rows16 ? size == 4 && g.K <= 256 : g.K <= 1280 * size;
+  return eight ? matmul_i8_pair<O, 8>(g, pair, sms, s) : matmul_i8_pair<O, 4>(g, pair, sms, s);
 }
 
 // The checks and launch that qbsa_rms_norm_quant and qbsa_quantize_token share.

@@ -394,6 +394,14 @@ def test_matmul_i8_sizes(m, n, k, dtype):
     _run_matmul(m * 7 + n, m, n, k, dtype, (m + n) % 2 == 0)
 
 
+@pytest.mark.parametrize("m,n,k", [(1100, 1031, 2560), (1100, 1031, 2576), (1100, 1031, 5120), (1100, 1031, 5136),
+                                   (2049, 1032, 256), (2049, 1032, 257), (2500, 640, 16), (1300, 1000, 1024)])
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+def test_matmul_i8_many_tokens_of_short_and_long_rows(m, n, k, dtype):
+    """Both numbers of epilogue warps, for outputs on and off 16-byte boundaries."""
+    _run_matmul(m + n + k, m, n, k, dtype, k % 32 == 0)
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_matmul_i8_largest_sums(m):
     """Every code at its extreme: the sum is 2^14 K, just below 2^31 at the largest K."""
