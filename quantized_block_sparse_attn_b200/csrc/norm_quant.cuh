@@ -307,14 +307,16 @@ __device__ __forceinline__ bool row_step(uint32_t a_bits, float& s, float& r) {
   return a_bits < 0x7f800000u;
 }
 
-// The row's scale.  sum = sum of (h * unit)^2, unit 1 unless the squares overflow.
+// The row's scale.  sum = sum of (h * unit)^2, unit 1 unless the squares overflow.  The root is then that
+// of the row times unit; a large s takes unit before the division and a small one after it, so that no
+// step leaves f32's range before the scale does.
 template <bool kNorm>
 __device__ __forceinline__ float row_scale(uint32_t a_bits, bool numbers, float s, float sum, float unit, int width,
                                            float eps) {
   if (!numbers) return __uint_as_float(0x7fc00000u);
   if (!kNorm || a_bits == 0) return s;
-  const float mean = __fdiv_rn(sum, static_cast<float>(width));
-  return __fdiv_rn(s, __fsqrt_rn(mean + eps * unit * unit)) * unit;
+  const float root = __fsqrt_rn(__fdiv_rn(sum, static_cast<float>(width)) + eps * unit * unit);
+  return s >= 1.0f ? __fdiv_rn(s * unit, root) : __fdiv_rn(s, root) * unit;
 }
 
 // h (stored, or staged at shared-memory address h_stage), its square sum, g and its largest
@@ -422,14 +424,17 @@ __device__ __forceinline__ void codes_of(const float (&g)[E], float s, float r, 
   }
 }
 
-// Squares that overflow in f32 (a finite row above about 1e19): the sum again, of h * 2^-64.
+// Squares that overflow in f32 (a finite row above about 1e19), or do so with eps: the sum again, of
+// h * 2^-96.  |h| < 2^128 and width <= 2^24 keep it at most 2^88, and what was above 2^127 stays above
+// 2^-65.
+constexpr float kOverflowUnit = 1.2621774483536189e-29f;  // 2^-96
 template <typename T, bool kRes>
 __device__ __noinline__ float sum_scaled(const NormQuantParams& p, int64_t row, int member, int step) {
   const T* h = kRes ? static_cast<const T*>(p.h_out) + row * p.h_stride
                     : static_cast<const T*>(p.x) + row * p.x_stride;
   float sum = 0.f;
   for (int i = member; i < p.width; i += step) {
-    const float v = to_f32(h[i]) * 5.421010862427522e-20f;
+    const float v = to_f32(h[i]) * kOverflowUnit;
     sum = __fmaf_rn(v, v, sum);
   }
   return sum;
@@ -450,8 +455,9 @@ __device__ __forceinline__ void write_codes(const NormQuantParams& p, int64_t ro
   }
 }
 
-constexpr float kOverflowUnit = 5.421010862427522e-20f;  // 2^-64
-__device__ __forceinline__ bool squares_overflow(bool numbers, float sum) { return numbers && !(sum <= 3.4e38f); }
+__device__ __forceinline__ bool squares_overflow(bool numbers, float sum, float eps) {
+  return numbers && !(sum + eps <= 3.4e38f);
+}
 
 // Narrow rows: p.group <= 32 threads per row, several rows per CTA, no barrier.  (A second row per
 // group with its loads in flight together cost more registers than it hid latency: 10.5 us against
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(256) norm_quant_rows_kernel(const __grid_const
   float s, r, unit = 1.f;
   const bool numbers = row_step(a, s, r);
   if constexpr (kNorm) {
-    const bool again = squares_overflow(numbers, sum);  // the same in a row's threads
+    const bool again = squares_overflow(numbers, sum, p.eps);  // the same in a row's threads
     if (__any_sync(0xffffffffu, again)) {
       __syncwarp();  // h of the row's other threads is written
       float small = again && live ? sum_scaled<T, kRes>(p, row, member, p.group) : 0.f;
@@ -527,7 +533,7 @@ __global__ void __launch_bounds__(kChunks * E > 16 ? 640 : 1024)
   row_reduce_cta<kNorm>(sum, a, 0);
   float s, r, unit = 1.f;
   const bool numbers = row_step(a, s, r);
-  if (kNorm && squares_overflow(numbers, sum)) {  // the same in every thread
+  if (kNorm && squares_overflow(numbers, sum, p.eps)) {  // the same in every thread
     __syncthreads();                               // h of the other threads is written
     sum = sum_scaled<T, kRes>(p, row, member, step);
     row_reduce_cta<kNorm>(sum, a, 1);
@@ -675,7 +681,7 @@ __global__ void __launch_bounds__(kChunks == 4 ? 640 : 512, kChunks == 4 ? 1 : 2
     }
     float width, r, unit = 1.f;
     const bool numbers = row_step(a, width, r);
-    if (kNorm && squares_overflow(numbers, sum)) {  // the same in every thread
+    if (kNorm && squares_overflow(numbers, sum, p.eps)) {  // the same in every thread
       __syncthreads();
       sum = sum_scaled<T, kRes>(p, row, tid, step);
       row_reduce_cta<kNorm>(sum, a, it & 1);
@@ -710,7 +716,7 @@ __global__ void __launch_bounds__(kNormWideThreads) norm_quant_wide_kernel(const
   row_reduce_cta<kNorm>(sum, a, 0);
   float s, r, unit = 1.f;
   const bool numbers = row_step(a, s, r);
-  if (kNorm && squares_overflow(numbers, sum)) {
+  if (kNorm && squares_overflow(numbers, sum, p.eps)) {
     __syncthreads();
     sum = sum_scaled<T, kRes>(p, row, threadIdx.x, kNormWideThreads);
     row_reduce_cta<kNorm>(sum, a, 1);
