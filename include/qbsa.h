@@ -234,7 +234,8 @@ typedef enum { QBSA_BF16 = 0, QBSA_FP16 = 1, QBSA_FP32 = 2 } qbsa_dtype;
  *               residual and residual_out are both given or both NULL; residual_out may be x
  *               or residual itself (same row stride), and overlaps nothing otherwise.
  *   weight      [width], of dtype or f32 (weight_dtype).
- *   eps         finite, above 0.
+ *   eps         finite, at least 2^-126 (next to a smaller one, squares below f32's normal range
+ *               would be the mean, without their lower bits).
  *   codes       int8 [rows, width] with row stride codes_stride >= width.  What lies between
  *               the rows is left as it was.  Rows that qbsa_matmul_i8 reads start at multiples
  *               of 16 bytes.

@@ -1062,7 +1062,8 @@ qbsa_status qbsa_rms_norm_quant(const void* x, int64_t x_stride, const void* res
   if (!aligned_to(weight, dtype_bytes(weight_dtype))) return fail(QBSA_ERR_INVALID, "weight is not aligned");
   if (rows != 0 && (residual == nullptr) != (residual_out == nullptr))
     return fail(QBSA_ERR_INVALID, "residual and residual_out are given together");
-  if (!std::isfinite(eps) || eps <= 0.f) return fail(QBSA_ERR_INVALID, "eps must be finite and above 0");
+  // squares below 2^-126 lose bits: next to a smaller eps they would be the mean
+  if (!std::isfinite(eps) || eps < 1.17549435e-38f) return fail(QBSA_ERR_INVALID, "eps must be finite and at least 2^-126");
   qbsa::NormQuantParams prm;
   memset(&prm, 0, sizeof(prm));
   prm.x = x;

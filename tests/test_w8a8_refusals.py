@@ -1,0 +1,33 @@
+"""CPU checks of calls that the 8-bit linear layers have to refuse, and of some that they have to take."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import quantized_block_sparse_attn_b200 as qb
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from quantized_block_sparse_attn_b200 import build
+    build.build()
+
+
+def _at(address):
+    return ctypes.c_void_p(address)
+
+
+def _norm(x=0x10000, xs=64, res=None, rs=0, w=0x900000, dt=0, wdt=0, rows=4, width=64, eps=1e-6, h=None, hs=0,
+          codes=0x20000, cs=64, scales=0x30000):
+    p = [None if a is None else _at(a) for a in (x, res, w, h, codes, scales)]
+    st = qb.lib().qbsa_rms_norm_quant(p[0], xs, p[1], rs, p[2], dt, wdt, rows, width, eps, p[3], hs, p[4], cs, p[5],
+                                      None)
+    return st, qb.lib().qbsa_last_error().decode()
+
+
+@pytest.mark.parametrize("eps", [1e-40, 1.4e-45, float(np.nextafter(np.float32(2.0 ** -126), np.float32(0)))])
+def test_an_eps_that_float32_does_not_hold_in_full_is_refused(eps):
+    """h^2 of h = 3e-23 is 9e-46, in float32 1.4e-45: 2 % of the norm next to an eps of 1e-44."""
+    st, msg = _norm(eps=eps)
+    assert st == 1 and "eps" in msg
