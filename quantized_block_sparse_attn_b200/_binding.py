@@ -306,13 +306,15 @@ def _rows(name, t):
         raise ValueError(f"{name} must be [..., width], contiguous in its last dimension")
     if len(shape) == 2:
         return shape[0], strides[0]
+    if 0 in shape[:-1]:
+        return 0, shape[-1]
     rows, stride = 1, shape[-1]
     for n, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if n == 1:
             continue
         if rows == 1:
             stride = st
-        elif n > 0 and st != stride * rows:
+        elif st != stride * rows:
             raise ValueError(f"{name}: its rows are not evenly spaced; make it contiguous")
         rows *= n
     return rows, stride

@@ -47,3 +47,20 @@ def test_mean_and_eps_that_overflow_together(width):
         codes, scales, _ = qb.rms_norm_quant(x, w, eps)
         qb.check()
         _check_tokens(codes, scales, x, w, float(torch.tensor(eps, dtype=FP32)))
+
+
+@pytest.mark.parametrize("lead", [(0,), (0, 3), (3, 0), (2, 0, 1), (2, 1, 0)])
+def test_empty_batches(lead):
+    """No tokens, wherever the empty dimension stands, with outputs made and given."""
+    x, w = torch.empty((*lead, 48), dtype=BF16, device="cuda"), _randn(2, (48,), BF16)
+    b, sb = qb.quantize_token(_randn(1, (40, 48), BF16))
+    for given in (False, True):
+        kw = dict(codes=torch.empty((*lead, 48), dtype=torch.int8, device="cuda"),
+                  scales=torch.empty(lead, device="cuda")) if given else {}
+        c, s, h = qb.rms_norm_quant(x, w, residual=x, residual_out=torch.empty_like(x) if given else None, **kw)
+        assert c.shape == x.shape and s.shape == lead and h.shape == x.shape
+        c, s = qb.quantize_token(x, **kw)
+        assert c.shape == x.shape and s.shape == lead
+        out = torch.empty((*lead, 40), dtype=BF16, device="cuda") if given else None
+        assert qb.matmul_i8(c, b, s, sb, out=out).shape == (*lead, 40)
+    qb.check()

@@ -4,8 +4,10 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import quantized_block_sparse_attn_b200 as qb
+from quantized_block_sparse_attn_b200 import _binding
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -31,3 +33,23 @@ def test_an_eps_that_float32_does_not_hold_in_full_is_refused(eps):
     """h^2 of h = 3e-23 is 9e-46, in float32 1.4e-45: 2 % of the norm next to an eps of 1e-44."""
     st, msg = _norm(eps=eps)
     assert st == 1 and "eps" in msg
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (0, 3, 64), (3, 0, 64), (3, 0, 1), (2, 1, 0, 64), (2, 0, 1, 64), (0, 0, 5)])
+def test_no_rows_wherever_the_empty_dimension_stands(shape):
+    t = torch.empty(shape)
+    assert _binding._rows("x", t)[0] == 0
+    assert _binding._rows("x", t.transpose(0, len(shape) - 2))[0] == 0
+    assert _binding._rows("x", torch.empty((4, *shape[1:-1], 70))[:0, ..., 3:67])[0] == 0
+
+
+def test_rows_evenly_spaced_or_refused():
+    x = torch.empty((4, 6, 80))
+    assert _binding._rows("x", x) == (24, 80)
+    assert _binding._rows("x", x[..., 3:70]) == (24, 80)
+    assert _binding._rows("x", x[:, :1]) == (4, 480)
+    assert _binding._rows("x", x[:1, ::2]) == (3, 160)
+    assert _binding._rows("x", x[0, 0]) == (1, 80)
+    for t in (x[:, :5], x.transpose(0, 1), x[..., ::2]):
+        with pytest.raises(ValueError):
+            _binding._rows("x", t)
