@@ -299,6 +299,9 @@ def _dtype_code(dtype):
     return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
 
 
+_INT_MAX = 2 ** 31 - 1  # sizes above it would reach the library's int arguments as their lower 32 bits
+
+
 def _rows(name, t):
     """(row count, row stride) of a tensor [..., width] whose rows are contiguous and evenly spaced."""
     shape, strides = t.shape, t.stride()
@@ -352,6 +355,8 @@ def _token_arguments(x, codes, scales):
         raise ValueError("x must be a CUDA tensor [..., width] of bfloat16, float16 or float32, width >= 1")
     rows, xs = _rows("x", x)
     width = shape[-1]
+    if width > _INT_MAX:
+        raise QbsaError(2, f"width above 2^31 - 1 ({width})")
     if codes is None:
         if width % 16 == 0 and x.is_contiguous():
             codes, cs = torch.empty_like(x, dtype=torch.int8), width
@@ -428,6 +433,8 @@ def matmul_i8(a, b, a_scale, b_scale, *, bias=None, out_dtype=None, out=None):
         raise ValueError("a must be [..., K] and b [N, K]")
     m, sa = _rows("a", a)
     n, sb = _rows("b", b)
+    if m > _INT_MAX or n > _INT_MAX or b_shape[1] > _INT_MAX:
+        raise QbsaError(2, f"M, N or K above 2^31 - 1 ({m}, {n}, {b_shape[1]})")
     f32 = torch.float32
     _vector("a_scale", a_scale, m, dev, f32)
     _vector("b_scale", b_scale, n, dev, f32)

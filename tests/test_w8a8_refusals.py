@@ -1,6 +1,7 @@
 """CPU checks of calls that the 8-bit linear layers have to refuse, and of some that they have to take."""
 
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -53,3 +54,26 @@ def test_rows_evenly_spaced_or_refused():
     for t in (x[:, :5], x.transpose(0, 1), x[..., ::2]):
         with pytest.raises(ValueError):
             _binding._rows("x", t)
+
+
+def _tensor(shape, dtype):
+    """What the binding asks of a CUDA tensor before it makes the outputs, for sizes that no test allocates."""
+    strides = [1]
+    for n in reversed(shape[1:]):
+        strides.append(strides[-1] * n)
+    strides = tuple(reversed(strides))
+    return types.SimpleNamespace(shape=shape, dtype=dtype, get_device=lambda: 0, stride=lambda: strides)
+
+
+@pytest.mark.parametrize("size", [2 ** 31, 2 ** 32 - 5, 2 ** 32 + 64, 2 ** 33 + 1])
+def test_sizes_that_a_c_int_would_take_for_others(size):
+    """2^32 + 64 values of a row would be passed as 64."""
+    w = _tensor((size,), torch.bfloat16)
+    for call in (lambda: qb.quantize_token(_tensor((1, size), torch.bfloat16)),
+                 lambda: qb.rms_norm_quant(_tensor((2, 3, size), torch.bfloat16), w)):
+        with pytest.raises(qb.QbsaError, match="width"):
+            call()
+    i8 = torch.int8
+    for m, n, k in ((size, 8, 16), (8, size, 16), (8, 8, size)):
+        with pytest.raises(qb.QbsaError, match="M, N or K"):
+            qb.matmul_i8(_tensor((m, k), i8), _tensor((n, k), i8), None, None)
