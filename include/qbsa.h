@@ -232,7 +232,7 @@ typedef enum { QBSA_BF16 = 0, QBSA_FP16 = 1, QBSA_FP32 = 2 } qbsa_dtype;
  * reproducible bit for bit.  A row with a NaN or an infinity in g gets codes 0, scale NaN.
  *   x, residual, residual_out   [rows, width] of dtype, with row strides in elements.
  *               residual and residual_out are both given or both NULL; residual_out may be x
- *               or residual itself (same row stride), and overlaps nothing otherwise.
+ *               or residual itself (same row stride).
  *   weight      [width], of dtype or f32 (weight_dtype).
  *   eps         finite, at least 2^-126 (next to a smaller one, squares below f32's normal range
  *               would be the mean, without their lower bits).
@@ -240,6 +240,8 @@ typedef enum { QBSA_BF16 = 0, QBSA_FP16 = 1, QBSA_FP32 = 2 } qbsa_dtype;
  *               the rows is left as it was.  Rows that qbsa_matmul_i8 reads start at multiples
  *               of 16 bytes.
  *   scales      f32 [rows].
+ * Otherwise no byte of an output's rows belongs to an input or to another output
+ * (QBSA_ERR_INVALID); rows may interleave, as columns of one buffer do.
  * Any alignment that the element type allows is taken; rows of all tensors on 16-byte
  * boundaries (codes: 8 for 16-bit types, 4 for f32) run faster.  1 <= width <= 2^24;
  * rows = 0 does nothing.  Asynchronous on `stream`, no scratch memory.
@@ -266,8 +268,8 @@ qbsa_status qbsa_quantize_token(const void* x, int64_t x_stride, qbsa_dtype dtyp
  *               bytes, multiples of 16 (of no account for a single row).  Any code in
  *               [-128, 127].  Bytes beyond K in a row are not used.
  *   a_scale     f32 [M], b_scale f32 [N], bias f32 [N] or NULL.
- *   out         [M, N] of out_dtype with row stride out_stride >= N in elements; overlaps no
- *               input.  What lies between the rows is left as it was.
+ *   out         [M, N] of out_dtype with row stride out_stride >= N in elements; its rows
+ *               overlap no input's (QBSA_ERR_INVALID).  What lies between the rows is left as it was.
  * 1 <= K <= 131071 (QBSA_ERR_UNSUPPORTED above: the sum would leave 32 bits); M = 0 or N = 0
  * does nothing.  Asynchronous on `stream`, no scratch memory.
  */

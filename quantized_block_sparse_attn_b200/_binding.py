@@ -384,7 +384,7 @@ def rms_norm_quant(x, weight, eps: float = 1e-6, *, residual=None, residual_out=
     (None without a residual).
 
     x, residual [..., width] bf16, fp16 or fp32 CUDA tensors with evenly spaced rows; weight [width] in x's
-    type or fp32.  residual_out may be x or residual itself.  New codes are laid out with rows at multiples
+    type or fp32.  residual_out may be x or residual itself; outputs share no memory otherwise.  New codes are laid out with rows at multiples
     of 16 bytes, as matmul_i8 reads them."""
     dev, code, codes, scales, rows, xs, cs = _token_arguments(x, codes, scales)
     width = x.shape[-1]
@@ -424,7 +424,7 @@ def matmul_i8(a, b, a_scale, b_scale, *, bias=None, out_dtype=None, out=None):
 
     a [..., K] and b [N, K] int8 CUDA tensors (16-byte aligned, rows at multiples of 16 bytes, as the
     quantisers lay them out), a_scale [...], b_scale [N] and bias [N] fp32.  out_dtype bf16 (default), fp16
-    or fp32; a given out [..., N] says it by its type."""
+    or fp32; a given out [..., N], which shares no memory with an input, says it by its type."""
     import torch
     dev, a_shape, b_shape = a.get_device(), a.shape, b.shape
     if dev < 0 or b.get_device() != dev or a.dtype != torch.int8 or b.dtype != torch.int8:

@@ -759,6 +759,36 @@ int dtype_bytes(qbsa_dtype t) { return t == QBSA_FP32 ? 4 : 2; }
 bool known_dtype(qbsa_dtype t) { return t == QBSA_BF16 || t == QBSA_FP16 || t == QBSA_FP32; }
 bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
+// Rows in memory: `rows` runs of `bytes`, `pitch` bytes apart.
+struct RowSpan {
+  const void* ptr;
+  int64_t rows, bytes, pitch;
+};
+
+// Whether a byte belongs to rows of both.  Rows may interleave (columns of one buffer).
+bool overlap(const RowSpan& a, const RowSpan& b) {
+  if (!a.ptr || !b.ptr) return false;
+  const int64_t a0 = reinterpret_cast<intptr_t>(a.ptr), b0 = reinterpret_cast<intptr_t>(b.ptr);
+  const int64_t ap = a.rows > 1 ? a.pitch : 0, bp = b.rows > 1 ? b.pitch : 0;
+  if (a0 + (a.rows - 1) * ap + a.bytes <= b0 || b0 + (b.rows - 1) * bp + b.bytes <= a0) return false;
+  auto floor_div = [](int64_t x, int64_t y) { return x >= 0 ? x / y : -((-x + y - 1) / y); };
+  // some row j < rows of x, at x0 + j * step, meets [lo, hi)
+  auto meets = [&](const RowSpan& x, int64_t x0, int64_t step, int64_t first, int64_t rows, int64_t lo, int64_t hi) {
+    if (step == 0) return lo < x0 + x.bytes && x0 < hi;
+    const int64_t from = std::max(first, floor_div(lo - x.bytes - x0, step) + 1);
+    const int64_t to = std::min(rows - 1, -floor_div(x0 - hi, step) - 1);
+    return from <= to;
+  };
+  // of one pitch: only the rows' distance i - j counts
+  if (ap == bp) return meets(a, a0, ap, 1 - b.rows, a.rows, b0, b0 + b.bytes);
+  const bool fewer = a.rows <= b.rows;
+  const RowSpan &f = fewer ? a : b, &o = fewer ? b : a;
+  const int64_t f0 = fewer ? a0 : b0, fp = fewer ? ap : bp, o0 = fewer ? b0 : a0, op = fewer ? bp : ap;
+  for (int64_t i = 0; i < f.rows; ++i)
+    if (meets(o, o0, op, 0, o.rows, f0 + i * fp, f0 + i * fp + f.bytes)) return true;
+  return false;
+}
+
 constexpr int kNormRingBytes = 216 * 1024;  // of an SM's shared memory, over its resident CTAs
 
 template <typename T, bool kNorm, bool kRes, int E, int kChunks>
@@ -1031,6 +1061,16 @@ qbsa_status norm_quant_impl(qbsa::NormQuantParams& prm, qbsa_dtype dtype, void* 
       return fail(QBSA_ERR_INVALID, "residual_out in place needs the row stride of the tensor that it replaces");
   }
   if (prm.rows == 0) return QBSA_OK;
+  const RowSpan x = {prm.x, prm.rows, (int64_t)prm.width * size, prm.x_stride * size},
+                residual = {prm.residual, prm.rows, x.bytes, prm.r_stride * size},
+                weight = {prm.weight, 1, (int64_t)prm.width * (prm.weight_f32 ? 4 : size), 0},
+                h_out = {prm.h_out, prm.rows, x.bytes, prm.h_stride * size},
+                codes = {prm.codes, prm.rows, prm.width, prm.c_stride}, scales = {prm.scales, 1, 4 * prm.rows, 0};
+  if ((prm.h_out != prm.x && overlap(h_out, x)) || (prm.h_out != prm.residual && overlap(h_out, residual)))
+    return fail(QBSA_ERR_INVALID, "residual_out overlaps an input that it does not replace");
+  bool shared = overlap(h_out, weight) || overlap(h_out, codes) || overlap(h_out, scales) || overlap(codes, scales);
+  for (const RowSpan* t : {&x, &residual, &weight}) shared = shared || overlap(codes, *t) || overlap(scales, *t);
+  if (shared) return fail(QBSA_ERR_INVALID, "outputs overlap an input or one another");
   // rows by 16-byte pieces where every row of every tensor starts on such a boundary
   const int piece = 16 / size;
   auto rows16 = [&](const void* ptr, int64_t stride) {
@@ -1118,6 +1158,11 @@ qbsa_status qbsa_matmul_i8(const int8_t* a, int64_t a_stride, const int8_t* b, i
     return fail(QBSA_ERR_INVALID, "scales, bias and out must be aligned to their element");
   if ((int64_t)((M + 255) / 256) * ((N + 63) / 64) > 0x3fffffffLL)
     return fail(QBSA_ERR_UNSUPPORTED, "too many output tiles");
+  const int size = dtype_bytes(out_dtype);
+  const RowSpan result = {out, M, (int64_t)N * size, out_stride * size};
+  for (const RowSpan& t : {RowSpan{a, M, K, a_stride}, RowSpan{b, N, K, b_stride}, RowSpan{a_scale, 1, 4ll * M, 0},
+                           RowSpan{b_scale, 1, 4ll * N, 0}, RowSpan{bias, 1, 4ll * N, 0}})
+    if (overlap(result, t)) return fail(QBSA_ERR_INVALID, "out overlaps an input");
   MatmulArgs g = {a, b, a_scale, b_scale, bias, out, M > 1 ? a_stride : (K + 15) / 16 * 16,
                   N > 1 ? b_stride : (K + 15) / 16 * 16, out_stride, M, N, K};
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -6,6 +6,7 @@ float32, terms = max(32, width / 1024 + 16).  A sum taken again of scaled values
 scaling is by a power of two, and what it pushes below float32's range is 2^-100 of the row's sum.
 """
 
+import numpy as np
 import pytest
 import torch
 
@@ -64,3 +65,62 @@ def test_empty_batches(lead):
         out = torch.empty((*lead, 40), dtype=BF16, device="cuda") if given else None
         assert qb.matmul_i8(c, b, s, sb, out=out).shape == (*lead, 40)
     qb.check()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_rows_that_interleave_or_overlap(dtype):
+    """Tensors laid out at random in one buffer: a call runs where no output meets another tensor, byte by
+    byte, and is refused where one does."""
+    rng = np.random.default_rng(5)
+    size = 2 if dtype == BF16 else 4
+    w = _randn(2, (24,), FP32)
+    ran = refused = 0
+    for _ in range(400):
+        rows, width = int(rng.integers(1, 6)), int(rng.integers(1, 25))
+        same = int(rng.integers(width, 60))                 # one pitch for all of them, half of the time
+        one = rng.random() < 0.5
+        buf = torch.from_numpy(rng.integers(0, 8, 4096).astype(np.uint8)).cuda()
+        at, held = {}, {}
+        for name, item, n in (("x", size, width), ("residual", size, width), ("h", size, width), ("codes", 1, width),
+                              ("scales", 4, rows)):
+            pitch = n if name == "scales" else (same if one else int(rng.integers(n, 60))) * (size if one else item) // item
+            count = 1 if name == "scales" else rows
+            start = int(rng.integers(0, 4096 // item - pitch * count))
+            if one and name != "scales" and name != "x" and rng.random() < 0.7:      # beside x, in its pitch
+                start = min(4096 // item - pitch * count, int(at["x"][0] + rng.integers(0, same * size)) // item)
+            at[name] = (start * item, pitch * item if count > 1 else 0, item * n, count)
+            view = buf.view({"scales": FP32, "codes": torch.int8}.get(name, dtype))
+            held[name] = view.as_strided((rows,) if name == "scales" else (rows, width),
+                                         (1,) if name == "scales" else (pitch, 1), start)
+
+        def bytes_of(name):
+            first, pitch, length, count = at[name]
+            return {first + i * pitch + j for i in range(count) for j in range(length)}
+
+        outs = [("h", "x"), ("h", "residual"), ("h", "codes"), ("h", "scales"), ("codes", "scales"), ("codes", "x"),
+                ("codes", "residual"), ("scales", "x"), ("scales", "residual")]
+        in_place = {n for n in ("x", "residual") if at[n][0] == at["h"][0]}
+        clash = any(bytes_of(a) & bytes_of(b) for a, b in outs if not (a == "h" and b in in_place and at[b] == at["h"]))
+        x, residual = held["x"].clone(), held["residual"].clone()
+        before = buf.clone()
+
+        def call():
+            return qb.rms_norm_quant(held["x"], w[:width], residual=held["residual"], residual_out=held["h"],
+                                     codes=held["codes"], scales=held["scales"])
+
+        if clash:
+            with pytest.raises(qb.QbsaError):
+                call()
+            assert torch.equal(buf, before)
+            refused += 1
+        else:
+            codes, scales, h = call()
+            want = qb.rms_norm_quant(x, w[:width], residual=residual)
+            assert torch.equal(codes, want[0]) and torch.equal(h, want[2])
+            assert torch.equal(scales.view(torch.int32), want[1].view(torch.int32))
+            keep = torch.ones(4096, dtype=torch.bool)
+            keep[sorted(bytes_of("h") | bytes_of("codes") | bytes_of("scales"))] = False
+            assert torch.equal(buf.cpu()[keep], before.cpu()[keep])
+            ran += 1
+    qb.check()
+    assert ran >= 40 and refused >= 40

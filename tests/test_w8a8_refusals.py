@@ -77,3 +77,34 @@ def test_sizes_that_a_c_int_would_take_for_others(size):
     for m, n, k in ((size, 8, 16), (8, size, 16), (8, 8, size)):
         with pytest.raises(qb.QbsaError, match="M, N or K"):
             qb.matmul_i8(_tensor((m, k), i8), _tensor((n, k), i8), None, None)
+
+
+@pytest.mark.parametrize("over", [
+    dict(codes=0x10000),                                            # codes over x
+    dict(codes=0x10000 + 3 * 128 + 126),                            # over the last row's last value
+    dict(codes=0x10000 + 127, xs=256, cs=640, rows=9),              # pitches that differ, in row 0's last byte
+    dict(scales=0x10000 + 8),
+    dict(scales=0x20000 + 12),                                      # scales over codes
+    dict(w=0x20000),
+    dict(scales=0x900000),
+    dict(res=0x40000, rs=64, h=0x40000 + 128, hs=64),               # a row further on
+    dict(res=0x40000, rs=64, h=0x10000 + 2, hs=64),                 # x, one value further on
+    dict(res=0x10000 + 128, rs=64, h=0x10000, hs=64),               # in place of x, and residual one row further on
+    dict(res=0x40000, rs=64, h=0x20000, hs=64),                     # residual_out over codes
+    dict(res=0x40000, rs=64, h=0x30000, hs=64),
+    dict(res=0x40000, rs=64, h=0x900000, hs=64),
+    dict(res=0x40000, rs=64, h=0x50000, hs=64, codes=0x40000 + 5),
+])
+def test_outputs_that_overlap(over):
+    st, msg = _norm(**over)
+    assert st == 1 and "overlap" in msg
+
+
+@pytest.mark.parametrize("over", [dict(out=0x10000), dict(out=0x20000 + 31 * 64 + 62), dict(out=0x30000 + 60),
+                                  dict(out=0x40000 + 124), dict(out=0x50000, bias=0x50000 + 16 * 64 - 4)])
+def test_products_over_their_inputs(over):
+    p = dict(a=0x10000, b=0x20000, sa=0x30000, sb=0x40000, bias=0x48000, out=0x50000)
+    p.update(over)
+    st = qb.lib().qbsa_matmul_i8(_at(p["a"]), 64, _at(p["b"]), 64, _at(p["sa"]), _at(p["sb"]), _at(p["bias"]), 16, 32,
+                                 64, 0, _at(p["out"]), 32, None)
+    assert st == 1 and b"overlaps" in qb.lib().qbsa_last_error()
