@@ -341,13 +341,22 @@ qbsa_status qbsa_block_topk_keep(const float* q_mean, const float* k_mean, int B
 
 /*
  * qbsa_wait_selftest -- test hook for failure detection (no counterpart on the source
- * pages): launches two threads that wait, each through one of the two bounded mbarrier waits
- * that the kernels of this library use, on phases that nothing ever completes.  After the wait
- * limit (2 s) each records a timeout in the device error word and the kernel ends normally,
- * so the next qbsa_check(stream) returns QBSA_ERR_TIMEOUT and the context stays usable.  No
- * fault, trap or endless loop is involved.
+ * pages): launches one thread that waits, through the bounded mbarrier wait that the
+ * attention kernels use, on a phase that nothing ever completes.  After the wait
+ * limit (2 s) the thread records a timeout in the device error word and the kernel ends
+ * normally, so the next qbsa_check(stream) returns QBSA_ERR_TIMEOUT and the context stays
+ * usable.  No fault, trap or endless loop is involved.
  */
 qbsa_status qbsa_wait_selftest(void* stream);
+
+/*
+ * qbsa_wait_selftest_form -- the same for one form of the wait at a time: 0 the wait of
+ * qbsa_wait_selftest, 1 the clean-up wait, which an abort does not end, 2 and 3 the suspended
+ * waits of the 8-bit linear layers on a barrier of the CTA and of the cluster.
+ *   result      device int64 [3]: 1 if the wait saw the phase complete (it must not), the
+ *               CTA's abort flag after it (raised by all forms but 1), and its nanoseconds.
+ */
+qbsa_status qbsa_wait_selftest_form(int form, int64_t* result, void* stream);
 
 /*
  * qbsa_check -- waits for `stream`, then reports and clears the device error word:

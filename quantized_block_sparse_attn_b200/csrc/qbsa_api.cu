@@ -1264,25 +1264,40 @@ qbsa_status qbsa_block_topk_keep(const float* q_mean, const float* k_mean, int B
 }
 
 namespace qbsa {
-// Failure-detection self-test: two threads wait, each through one of the kernels' bounded waits, on
-// mbarrier phases that nothing completes; the waits give up after their time limit, record the
-// timeout in the device error word and the kernel returns normally.
-__global__ void wait_selftest_kernel() {
-  __shared__ uint64_t barrier[2];
-  __shared__ int abort_flag[2];
-  const int i = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) != 0) return;
-  abort_flag[i] = 0;
-  const uint32_t bar = smem_u32(&barrier[i]);
+// Failure-detection self-test: one thread waits, through one of the kernels' own bounded waits, on
+// an mbarrier phase that nothing completes; the wait gives up after its time limit, records
+// the timeout in the device error word and the kernel returns normally.  `result`, if given: what the
+// wait returned, the abort flag after it and its nanoseconds.
+__global__ void wait_selftest_kernel(int form, int64_t* result) {
+  __shared__ uint64_t barrier;
+  __shared__ int abort_flag;
+  if (threadIdx.x != 0) return;
+  abort_flag = 0;
+  const uint32_t bar = smem_u32(&barrier);
   mbar_init(bar, 1);
   fence_mbar_init();
-  if (i == 0) mbar_wait(bar, 0, &abort_flag[i]);  // no arrival ever comes
-  else mbar_wait_hot(bar, 0, &abort_flag[i]);
+  const uint64_t t0 = global_timer_ns();
+  bool done;  // no arrival ever comes
+  if (form == 0) done = mbar_wait(bar, 0, &abort_flag);
+  else if (form == 1) done = mbar_wait_drain(bar, 0);
+  else if (form == 2) done = mbar_wait_hot(bar, 0, &abort_flag);
+  else done = mbar_wait_hot<true>(bar, 0, &abort_flag);
+  if (!result) return;
+  result[0] = done;
+  result[1] = *static_cast<volatile int*>(&abort_flag);
+  result[2] = static_cast<int64_t>(global_timer_ns() - t0);
 }
 }  // namespace qbsa
 
 qbsa_status qbsa_wait_selftest(void* stream) {
-  qbsa::wait_selftest_kernel<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>();
+  qbsa::wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(0, nullptr);
+  return check_launch("wait_selftest_kernel launch");
+}
+
+qbsa_status qbsa_wait_selftest_form(int form, int64_t* result, void* stream) {
+  if (form < 0 || form > 3) return fail(QBSA_ERR_INVALID, "form must be 0 to 3");
+  if (!result || !aligned_to(result, 8)) return fail(QBSA_ERR_INVALID, "result must be non-null and 8-byte aligned");
+  qbsa::wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(form, result);
   return check_launch("wait_selftest_kernel launch");
 }
 

@@ -108,3 +108,8 @@ def test_products_over_their_inputs(over):
     st = qb.lib().qbsa_matmul_i8(_at(p["a"]), 64, _at(p["b"]), 64, _at(p["sa"]), _at(p["sb"]), _at(p["bias"]), 16, 32,
                                  64, 0, _at(p["out"]), 32, None)
     assert st == 1 and b"overlaps" in qb.lib().qbsa_last_error()
+
+
+def test_wait_selftest_refusals():
+    for form, result in ((-1, 0x10000), (4, 0x10000), (0, None), (2, 0x10004)):
+        assert qb.lib().qbsa_wait_selftest_form(form, result, None) == 1
