@@ -24,6 +24,7 @@
 
 #include "ptx_cluster.cuh"
 #include "quantize.cuh"
+#include "stream_plan.h"
 
 namespace qbsa {
 
@@ -46,7 +47,6 @@ struct NormQuantParams {
 };
 
 constexpr int kNormWideThreads = 1024;
-constexpr int kNormMaxStages = 4;
 
 // Shared memory of a row in norm_quant_stream_kernel: its 16-byte pieces, and one unit more where
 // the row does not start on a unit's boundary.

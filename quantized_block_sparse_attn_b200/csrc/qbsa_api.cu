@@ -789,8 +789,6 @@ bool overlap(const RowSpan& a, const RowSpan& b) {
   return false;
 }
 
-constexpr int kNormRingBytes = 216 * 1024;  // of an SM's shared memory, over its resident CTAs
-
 template <typename T, bool kNorm, bool kRes, int E, int kChunks>
 qbsa_status launch_norm_rows(qbsa::NormQuantParams& prm, int values, cudaStream_t s) {
   prm.group = 1;
@@ -811,23 +809,25 @@ qbsa_status launch_norm_stream(qbsa::NormQuantParams& prm, int threads, cudaStre
   const int64_t slot = qbsa::stream_slot_bytes<T>(prm.width, kAligned);
   const int64_t stage = slot * (kRes ? 2 : 1), staged = kRes && !kAligned ? 2 * slot : 0;
   const auto kernel = qbsa::norm_quant_stream_kernel<T, kNorm, kRes, kChunks, kAligned>;
-  static std::atomic<int> resident{0};  // threads of an SM by the kernel's registers
-  if (resident.load(std::memory_order_relaxed) == 0) {
+  // threads of an SM by the kernel's registers, and its static shared memory (in the upper half)
+  static std::atomic<int64_t> attributes{0};
+  int64_t at = attributes.load(std::memory_order_relaxed);
+  if (at == 0) {
     cudaFuncAttributes fa;
     const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
     // each of an SM's four partitions holds whole warps of 8-register granules
     const int warps = 16384 / (32 * ((std::max(fa.numRegs, 1) + 7) / 8 * 8));
-    resident.store(128 * std::max(1, std::min(16, warps)), std::memory_order_relaxed);
+    at = (static_cast<int64_t>(fa.sharedSizeBytes) << 32) | (128 * std::max(1, std::min(16, warps)));
+    attributes.store(at, std::memory_order_relaxed);
   }
-  int per_sm = std::max(1, std::min(32, resident.load(std::memory_order_relaxed) / threads));
-  while (per_sm > 1 && (2 * stage + staged) * per_sm > kNormRingBytes) --per_sm;
-  prm.stages = static_cast<int>(std::min<int64_t>(qbsa::kNormMaxStages, (kNormRingBytes / per_sm - staged) / stage));
-  if (prm.stages < 2 || prm.rows <= (int64_t)sms * per_sm) return QBSA_OK;
+  const qbsa::StreamPlan plan = qbsa::plan_stream(static_cast<int>(at & 0xffffffff), threads, stage, staged, at >> 32);
+  prm.stages = plan.stages;
+  if (plan.stages < 2 || prm.rows <= (int64_t)sms * plan.per_sm) return QBSA_OK;
   if (!kAligned && (prm.x_stride < prm.width || (kRes && prm.r_stride < prm.width))) return QBSA_OK;
   static std::atomic<uint64_t> done{0};
-  if ((st = set_smem_once(kernel, kNormRingBytes, done)) != QBSA_OK) return st;
-  kernel<<<static_cast<unsigned>(sms) * per_sm, threads, static_cast<size_t>(prm.stages * stage + staged), s>>>(prm);
+  if ((st = set_smem_once(kernel, qbsa::kNormRingBytes, done)) != QBSA_OK) return st;
+  kernel<<<static_cast<unsigned>(sms) * plan.per_sm, threads, static_cast<size_t>(plan.smem), s>>>(prm);
   *taken = true;
   return check_launch("norm_quant_stream_kernel launch");
 }
