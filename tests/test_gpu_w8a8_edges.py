@@ -124,3 +124,78 @@ def test_rows_that_interleave_or_overlap(dtype):
             ran += 1
     qb.check()
     assert ran >= 40 and refused >= 40
+
+
+def _view(rows, width, pitch, off, dtype, seed=None, fill=None):
+    """A buffer with a margin at either end, and rows of it `pitch` apart from `off` on."""
+    buf = torch.full((off + rows * pitch + 40,), fill, dtype=dtype, device="cuda") if seed is None else \
+        _randn(seed, (off + rows * pitch + 40,), dtype)
+    return buf, buf.as_strided((rows, width), (pitch, 1), off)
+
+
+def _same_outside(buf, keep, view):
+    inside = torch.zeros(buf.numel(), dtype=torch.bool, device="cuda")
+    inside.as_strided(view.shape, view.stride(), view.storage_offset())[...] = True
+    return torch.equal(buf[~inside], keep[~inside])
+
+
+@pytest.mark.parametrize("width,pitches,offs", [
+    (264, (272, 280, 288, 304), (8, 16, 0, 16)),            # rows on 16-byte boundaries, with gaps
+    (520, (528, 520, 1040, 528), (0, 8, 24, 32)),
+    (264, (271, 269, 267, 265), (3, 5, 7, 1)),              # every row at another alignment
+    (265, (265, 266, 268, 272), (0, 1, 2, 16)),
+    (520, (521, 520, 523, 520), (1, 0, 4, 0)),              # one of them aligned
+    (1031, (1033, 1040, 1037, 1033), (2, 9, 5, 3)),
+    (1288, (1300, 1288, 1290, 1312), (6, 8, 2, 16)),
+    (4099, (4101, 4111, 4100, 4112), (7, 1, 3, 5)),
+    (9001, (9003, 9008, 9001, 9008), (1, 8, 0, 32)),        # four pieces per thread
+])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_many_rows_with_gaps_between_them(width, pitches, offs, dtype):
+    """The streamed kernels on rows of four different pitches and offsets: values, and what lies between the
+    rows and around them; the quantiser alone; the sum in place of either input."""
+    rows = 2500
+    xb, x = _view(rows, width, pitches[0], offs[0], dtype, seed=1)
+    rb, res = _view(rows, width, pitches[1], offs[1], dtype, seed=2)
+    w = _randn(3, (width,), dtype)
+    hb, h = _view(rows, width, pitches[2], offs[2], dtype, fill=7.0)
+    cb, codes = _view(rows, width, pitches[3], offs[3], torch.int8, fill=77)
+    keep = [t.clone() for t in (xb, rb, hb, cb)]
+    want = (x.float() + res.float()).to(dtype)
+    _, scales, got = qb.rms_norm_quant(x, w, residual=res, residual_out=h, codes=codes)
+    qb.check()
+    assert got.data_ptr() == h.data_ptr() and torch.equal(h, want)
+    _check_tokens(codes, scales, want, w, 1e-6)
+    assert torch.equal(xb, keep[0]) and torch.equal(rb, keep[1])
+    assert _same_outside(hb, keep[2], h) and _same_outside(cb, keep[3], codes)
+    first = codes.clone()
+    for kw in (dict(residual=None), dict(residual=res, residual_out=res), dict(residual=res, residual_out=x)):
+        if kw["residual"] is not None and kw["residual_out"] is x:
+            rb.copy_(keep[1])
+        codes.fill_(55)
+        _, s, _ = qb.rms_norm_quant(x, w, codes=codes, **kw)
+        qb.check()
+        if kw["residual"] is None:
+            _check_tokens(codes, s, x, w, 1e-6)
+        else:
+            assert torch.equal(codes, first) and torch.equal(s, scales) and torch.equal(kw["residual_out"], want)
+        assert _same_outside(xb, keep[0], x) and _same_outside(rb, keep[1], res) and _same_outside(cb, keep[3], codes)
+    xb.copy_(keep[0])
+    _, s = qb.quantize_token(x, codes=codes)
+    qb.check()
+    _check_tokens(codes, s, x)
+    assert torch.equal(xb, keep[0]) and _same_outside(cb, keep[3], codes)
+
+
+def test_columns_of_one_buffer():
+    """x, the sum and the residual as columns of one buffer, many rows: outputs and inputs share 16-byte units."""
+    rows, width = 2500, 527
+    buf = _randn(1, (rows, 3 * width), BF16)
+    keep = buf.clone()
+    x, h, res = buf[:, :width], buf[:, width:2 * width], buf[:, 2 * width:]
+    w = _randn(2, (width,), BF16)
+    codes, scales, _ = qb.rms_norm_quant(x, w, residual=res, residual_out=h)
+    qb.check()
+    want = (keep[:, :width].float() + keep[:, 2 * width:].float()).to(BF16)
+    assert torch.equal(h, want) and torch.equal(x, keep[:, :width]) and torch.equal(res, keep[:, 2 * width:])
+    _check_tokens(codes, scales, want, w, 1e-6)
