@@ -386,7 +386,8 @@ __device__ __forceinline__ void take_values(const NormQuantParams& p, int64_t ro
 // warps into the slow branch (97 us against 60 at 16384 x 5120).  Their quotient is taken with
 // 1 / s in two parts instead, r and RN(r RN(1 - s r)): FMA(x, r, RN(x r_low)) equals RN(x / s) for
 // every significand of x and a that bf16 or fp16 have and every ratio up to 2^8 (tested over all
-// of them; beyond that the code is 0), and powers of two only scale it while r_low is normal.
+// of them, on the host and here; beyond that the code is 0).  Powers of two only scale it while r_low
+// is normal; above that, up to the limit of 1.2e27 for s, bf16 is tested in the same way.
 template <bool kFew, int E>
 __device__ __forceinline__ void codes_of(const float (&g)[E], float s, float r, uint32_t (&code)[E]) {
   const float2 magic = make_float2(12582912.0f, 12582912.0f);

@@ -199,3 +199,21 @@ def test_columns_of_one_buffer():
     want = (keep[:, :width].float() + keep[:, 2 * width:].float()).to(BF16)
     assert torch.equal(h, want) and torch.equal(x, keep[:, :width]) and torch.equal(res, keep[:, 2 * width:])
     _check_tokens(codes, scales, want, w, 1e-6)
+
+
+@pytest.mark.parametrize("dtype,exponents", [(FP16, (0, 5, -8, -14, -20, -24)),
+                                             (BF16, (0, -100, -126, -127, -130, 88, 89, 90, 100, 119))])
+def test_quotients_of_every_maximum(dtype, exponents):
+    """Rows of a 16-bit type for every significand of the largest value, with every smaller significand at every
+    exponent that reaches a code; at scales where the step meets 2^-126, where it passes 1.2e27 (the two ways
+    of the quotient), and where the row is subnormal."""
+    n = 128 if dtype == BF16 else 1024
+    tops = torch.arange(n, 2 * n, device="cuda", dtype=torch.float32)
+    all_x = torch.cat([tops * 2.0 ** -j for j in range(9)])
+    rows = torch.where(all_x[None] <= tops[:, None], all_x[None], torch.zeros((), device="cuda"))
+    rows = torch.cat([tops[:, None], rows], 1)
+    for e in exponents:
+        x = (rows.double() * 2.0 ** e).to(dtype)
+        codes, scales = qb.quantize_token(x)
+        qb.check()
+        _check_tokens(codes, scales, x)
