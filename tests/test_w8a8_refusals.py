@@ -113,3 +113,8 @@ def test_products_over_their_inputs(over):
 def test_wait_selftest_refusals():
     for form, result in ((-1, 0x10000), (4, 0x10000), (0, None), (2, 0x10004)):
         assert qb.lib().qbsa_wait_selftest_form(form, result, None) == 1
+
+
+def test_version_tells_of_these_entry_points():
+    """Every addition of entry points has marked a version of its own; 1.03 did not have these."""
+    assert qb.lib().qbsa_version() >= 104
