@@ -118,3 +118,40 @@ def test_wait_selftest_refusals():
 def test_version_tells_of_these_entry_points():
     """Every addition of entry points has marked a version of its own; 1.03 did not have these."""
     assert qb.lib().qbsa_version() >= 104
+
+
+@pytest.mark.parametrize("short", [True, False])
+def test_calls_with_and_without_torch_s_short_names(monkeypatch, short):
+    """The stream and the device come from torch's public calls where the short ones are missing; a call for
+    another device than the current one makes that one current."""
+    if short:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 1000 + dev, raising=False)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+        monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: types.SimpleNamespace(cuda_stream=1000 + dev))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    entered = []
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            entered.append(self.dev)
+
+        def __exit__(self, *a):
+            entered.append(None)
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    _binding._stream_calls.cache_clear()
+    try:
+        seen = []
+        _binding._call_on(1, lambda *a: seen.append((a, list(entered))) or 0, "x")
+        _binding._call_on(3, lambda *a: seen.append((a, list(entered))) or 0, "y")
+        assert seen == [(("x", 1001), []), (("y", 1003), [3])] and entered == [3, None]
+        with pytest.raises(qb.QbsaError):
+            _binding._call_on(1, lambda *a: 1)
+    finally:
+        _binding._stream_calls.cache_clear()
