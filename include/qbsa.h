@@ -368,10 +368,11 @@ qbsa_status qbsa_check(void* stream);
 /* Thread-local description of the last non-OK status returned on this thread. */
 const char* qbsa_last_error(void);
 
-/* Library ABI version (major * 100 + minor): 104 (1.01 added qbsa_block_mean, qbsa_block_topk,
+/* Library ABI version (major * 100 + minor): 103 (1.01 added qbsa_block_mean, qbsa_block_topk,
  * qbsa_wait_selftest; 1.02 qbsa_block_topk_keep and qbsa_quantize_v_noalloc; 1.03
- * qbsa_fwd_host; 1.04 qbsa_rms_norm_quant, qbsa_quantize_token, qbsa_matmul_i8 and
- * qbsa_wait_selftest_form). */
+ * qbsa_fwd_host).  qbsa_rms_norm_quant, qbsa_quantize_token, qbsa_matmul_i8 and
+ * qbsa_wait_selftest_form only add symbols to 1.03; a caller that must know asks for the
+ * symbol. */
 int qbsa_version(void);
 
 #ifdef __cplusplus

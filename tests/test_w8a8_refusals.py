@@ -115,11 +115,6 @@ def test_wait_selftest_refusals():
         assert qb.lib().qbsa_wait_selftest_form(form, result, None) == 1
 
 
-def test_version_tells_of_these_entry_points():
-    """Every addition of entry points has marked a version of its own; 1.03 did not have these."""
-    assert qb.lib().qbsa_version() >= 104
-
-
 @pytest.mark.parametrize("short", [True, False])
 def test_calls_with_and_without_torch_s_short_names(monkeypatch, short):
     """The stream and the device come from torch's public calls where the short ones are missing; a call for
