@@ -44,6 +44,7 @@ struct NormQuantParams {
   int codes_vec;   // rows of codes on boundaries of a piece's codes
   int stages;  // rows in flight per CTA (norm_quant_stream_kernel)
   float eps;
+  float square_limit;  // a row's sum of squares is taken again of scaled values above it
 };
 
 constexpr int kNormWideThreads = 1024;
@@ -307,16 +308,14 @@ __device__ __forceinline__ bool row_step(uint32_t a_bits, float& s, float& r) {
   return a_bits < 0x7f800000u;
 }
 
-// The row's scale.  sum = sum of (h * unit)^2, unit 1 unless the squares overflow.  The root is then that
-// of the row times unit; a large s takes unit before the division and a small one after it, so that no
-// step leaves f32's range before the scale does.
+// The row's scale.  sum = sum of (h * unit)^2, unit 1 unless the squares overflow.
 template <bool kNorm>
 __device__ __forceinline__ float row_scale(uint32_t a_bits, bool numbers, float s, float sum, float unit, int width,
                                            float eps) {
   if (!numbers) return __uint_as_float(0x7fc00000u);
   if (!kNorm || a_bits == 0) return s;
   const float root = __fsqrt_rn(__fdiv_rn(sum, static_cast<float>(width)) + eps * unit * unit);
-  return s >= 1.0f ? __fdiv_rn(s * unit, root) : __fdiv_rn(s, root) * unit;
+  return __fdiv_rn(s, root) * unit;
 }
 
 // h (stored, or staged at shared-memory address h_stage), its square sum, g and its largest
@@ -425,9 +424,8 @@ __device__ __forceinline__ void codes_of(const float (&g)[E], float s, float r, 
   }
 }
 
-// Squares that overflow in f32 (a finite row above about 1e19), or do so with eps: the sum again, of
-// h * 2^-96.  |h| < 2^128 and width <= 2^24 keep it at most 2^88, and what was above 2^127 stays above
-// 2^-65.
+// Squares that overflow in f32 (a finite row above about 1e19): the sum again, of h * 2^-96.  |h| < 2^128
+// and width <= 2^24 keep it at most 2^88.
 constexpr float kOverflowUnit = 1.2621774483536189e-29f;  // 2^-96
 template <typename T, bool kRes>
 __device__ __noinline__ float sum_scaled(const NormQuantParams& p, int64_t row, int member, int step) {
@@ -456,8 +454,19 @@ __device__ __forceinline__ void write_codes(const NormQuantParams& p, int64_t ro
   }
 }
 
-__device__ __forceinline__ bool squares_overflow(bool numbers, float sum, float eps) {
-  return numbers && !(sum + eps <= 3.4e38f);
+// Such a row's (sum, unit) for row_scale: both are raised by the power of two that brings the larger of sum
+// and eps to about 2^120.  The root is then between 2^47 and 2^61, so that s / root, with s below 2^122,
+// does not overflow, and the unit at most 1, so that it loses no bits that the scale has.  (Choosing in
+// row_scale whether s or the quotient takes the unit, or comparing sum + eps with the limit, cost every
+// row 1 %: its thread is the one that the others of the CTA wait for.)
+__device__ __noinline__ float2 raise_sum(float sum, float eps) {
+  const float larger = fmaxf(sum, eps * kOverflowUnit * kOverflowUnit);
+  const int exponent = static_cast<int>(__float_as_uint(larger) >> 23) - 127;  // -70 to 88
+  const float f = __uint_as_float(static_cast<uint32_t>(127 + (120 - exponent) / 2) << 23);
+  return make_float2(sum * f * f, kOverflowUnit * f);
+}
+__device__ __forceinline__ bool squares_overflow(bool numbers, float sum, float limit) {
+  return numbers && !(sum <= limit);
 }
 
 // Narrow rows: p.group <= 32 threads per row, several rows per CTA, no barrier.  (A second row per
@@ -490,15 +499,14 @@ __global__ void __launch_bounds__(256) norm_quant_rows_kernel(const __grid_const
   float s, r, unit = 1.f;
   const bool numbers = row_step(a, s, r);
   if constexpr (kNorm) {
-    const bool again = squares_overflow(numbers, sum, p.eps);  // the same in a row's threads
+    const bool again = squares_overflow(numbers, sum, p.square_limit);  // the same in a row's threads
     if (__any_sync(0xffffffffu, again)) {
       __syncwarp();  // h of the row's other threads is written
       float small = again && live ? sum_scaled<T, kRes>(p, row, member, p.group) : 0.f;
       row_reduce_group<kNorm>(p.group, small, a);
-      if (again) {
-        sum = small;
-        unit = kOverflowUnit;
-      }
+      const float2 raised = raise_sum(small, p.eps);  // in every lane: behind a second branch 1 % slower
+      sum = again ? raised.x : sum;
+      unit = again ? raised.y : unit;
     }
   }
   if (!live) return;
@@ -534,11 +542,13 @@ __global__ void __launch_bounds__(kChunks * E > 16 ? 640 : 1024)
   row_reduce_cta<kNorm>(sum, a, 0);
   float s, r, unit = 1.f;
   const bool numbers = row_step(a, s, r);
-  if (kNorm && squares_overflow(numbers, sum, p.eps)) {  // the same in every thread
+  if (kNorm && squares_overflow(numbers, sum, p.square_limit)) {  // the same in every thread
     __syncthreads();                               // h of the other threads is written
     sum = sum_scaled<T, kRes>(p, row, member, step);
     row_reduce_cta<kNorm>(sum, a, 1);
-    unit = kOverflowUnit;
+    const float2 raised = raise_sum(sum, p.eps);
+    sum = raised.x;
+    unit = raised.y;
   }
   if (member == 0) p.scales[row] = row_scale<kNorm>(a, numbers, s, sum, unit, p.width, p.eps);
   write_codes<T, kNorm, E, kChunks>(p, row, member, step, g, numbers, s, r);
@@ -682,11 +692,13 @@ __global__ void __launch_bounds__(kChunks == 4 ? 640 : 512, kChunks == 4 ? 1 : 2
     }
     float width, r, unit = 1.f;
     const bool numbers = row_step(a, width, r);
-    if (kNorm && squares_overflow(numbers, sum, p.eps)) {  // the same in every thread
+    if (kNorm && squares_overflow(numbers, sum, p.square_limit)) {  // the same in every thread
       __syncthreads();
       sum = sum_scaled<T, kRes>(p, row, tid, step);
       row_reduce_cta<kNorm>(sum, a, it & 1);
-      unit = kOverflowUnit;
+      const float2 raised = raise_sum(sum, p.eps);
+      sum = raised.x;
+      unit = raised.y;
       __syncthreads();
     }
     if (tid == 0) p.scales[row] = row_scale<kNorm>(a, numbers, width, sum, unit, p.width, p.eps);
@@ -717,11 +729,13 @@ __global__ void __launch_bounds__(kNormWideThreads) norm_quant_wide_kernel(const
   row_reduce_cta<kNorm>(sum, a, 0);
   float s, r, unit = 1.f;
   const bool numbers = row_step(a, s, r);
-  if (kNorm && squares_overflow(numbers, sum, p.eps)) {
+  if (kNorm && squares_overflow(numbers, sum, p.square_limit)) {
     __syncthreads();
     sum = sum_scaled<T, kRes>(p, row, threadIdx.x, kNormWideThreads);
     row_reduce_cta<kNorm>(sum, a, 1);
-    unit = kOverflowUnit;
+    const float2 raised = raise_sum(sum, p.eps);
+    sum = raised.x;
+    unit = raised.y;
   }
   if (threadIdx.x == 0) p.scales[row] = row_scale<kNorm>(a, numbers, s, sum, unit, p.width, p.eps);
   const T* h = kRes ? static_cast<const T*>(p.h_out) + row * p.h_stride

@@ -1120,6 +1120,8 @@ qbsa_status qbsa_rms_norm_quant(const void* x, int64_t x_stride, const void* res
   prm.width = width;
   prm.weight_f32 = weight_dtype == QBSA_FP32;
   prm.eps = eps;
+  // mean + eps stays in range while the sum does; an eps that large needs every row scaled
+  prm.square_limit = eps < 1e37f ? 3.2e38f : -1.0f;
   return norm_quant_impl(prm, dtype, stream);
 }
 

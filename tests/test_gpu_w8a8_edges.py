@@ -11,7 +11,8 @@ import pytest
 import torch
 
 import quantized_block_sparse_attn_b200 as qb
-from tests.test_gpu_w8a8 import BF16, FP16, FP32, _check_tokens, _randn
+from oracle import linear8
+from tests.test_gpu_w8a8 import BF16, FP16, FP32, U, _check_tokens, _np, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -48,6 +49,27 @@ def test_mean_and_eps_that_overflow_together(width):
         codes, scales, _ = qb.rms_norm_quant(x, w, eps)
         qb.check()
         _check_tokens(codes, scales, x, w, float(torch.tensor(eps, dtype=FP32)))
+
+
+@pytest.mark.parametrize("rows,width", [(6, 1), (6, 72), (6, 1031), (6, 5120), (6, 33000), (2500, 1024), (2500, 1031)])
+@pytest.mark.parametrize("weight", [1e12, 1e-10, 1e-25])
+def test_large_rows_with_weights_far_from_one(rows, width, weight):
+    """Squares that overflow next to steps from 1e35 down to 1e-14 and below."""
+    for dtype in (BF16, FP32):
+        x = _randn(width, (rows, width), dtype)
+        x[0] = 1e20
+        x[1] = (x[1].float().sign() * 1e25).to(dtype)
+        x[2] = 1.8e19
+        w = torch.full((width,), weight, device="cuda")
+        for eps in (1e-6, 1e20, 1e36, 2e37, 3e38):
+            codes, scales, _ = qb.rms_norm_quant(x, w, eps)
+            qb.check()
+            assert np.array_equal(codes.cpu().numpy(), linear8.token_codes_f32(_np(x), _np(w)))
+            want = linear8.token_scales(_np(x), _np(w), float(torch.tensor(eps, dtype=FP32)))
+            bound = ((max(32, width / 1024 + 16) + 10) / 2 + 6) * U * 1.01 * want
+            # a scale below 2^-126 has steps of 2^-149: its quotient and the product with the unit, at most 1,
+            # are each rounded to half of one
+            assert np.all(np.abs(_np(scales) - want) <= bound + np.where(want < 2.0 ** -126, 2.0 ** -149, 0))
 
 
 @pytest.mark.parametrize("lead", [(0,), (0, 3), (3, 0), (2, 0, 1), (2, 1, 0)])
