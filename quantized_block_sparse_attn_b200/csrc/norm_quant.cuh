@@ -379,10 +379,11 @@ __device__ __forceinline__ void take_values(const NormQuantParams& p, int64_t ro
 // Codes of E values: rint_half_even(RN(g / s)), with r = RN(1 / s).
 //
 // In general as int8_code_byte: both ends of each quotient's bracket are rounded, and the values
-// are taken one by one if any of them differ.  That is rare for products with a weight, but not
-// for 16-bit values alone (kFew): both x and a are short there, so that x / s often is a
-// half-integer up to s's own rounding (about one value in a hundred of bf16), which sent most
-// warps into the slow branch (97 us against 60 at 16384 x 5120).  Their quotient is taken with
+// are taken one by one if any of them differ.  That is rare for products with a weight (unless the
+// weight is as short: 87 us for ones, 69 else, at 16384 x 5120), but not for 16-bit values alone
+// (kFew): both x and a are short there, so that x / s often is a half-integer up to s's own rounding
+// (about one value in a hundred of bf16), which sent most warps into the slow branch (65 us against 49
+// at 16384 x 5120, both streamed with two pieces per thread).  Their quotient is taken with
 // 1 / s in two parts instead, r and RN(r RN(1 - s r)): FMA(x, r, RN(x r_low)) equals RN(x / s) for
 // every significand of x and a that bf16 or fp16 have and every ratio up to 2^8 (tested over all
 // of them, on the host and here; beyond that the code is 0).  Powers of two only scale it while r_low

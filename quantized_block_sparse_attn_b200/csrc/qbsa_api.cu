@@ -1020,7 +1020,9 @@ qbsa_status matmul_i8_rows(const MatmulArgs& g, int sms, cudaStream_t s) {
   return check_launch("matmul_i8_rows_kernel launch");
 }
 
-// Up to 8 tokens: warp-level MMAs.  Else the tensor-core kernel that the plans find faster.  The pair
+// Up to 8 tokens: warp-level MMAs (against the split kernel at N, K in {1024, 5120, 20480}: 1 token 2.3 to 22.0
+// us, split 4.5 to 24.5; 8 tokens 2.5 to 23.7, split 4.8 to 24.9; slower only at K = 20480 with N from 5120 on, by
+// 0 to 14 %).  Else the tensor-core kernel that the plans find faster.  The pair
 // kernel takes eight epilogue warps instead of four (and a stage less) where a tile's multiplication
 // is too short to hide four.  Rows of out at any alignment are stored unit by unit, so there that lasts
 // to a K of 1280 per byte of O (eight against four, 4000 x 5003 x K: K = 2000 fp32 63.5 us against 70.0
